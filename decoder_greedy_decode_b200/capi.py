@@ -6,6 +6,7 @@ import of this module's functions raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -18,7 +19,15 @@ DEC_KV_FP8_E4M3 = 1
 DEC_DEV_BAD_POSITION = 1
 DEC_DEV_BAD_TOKEN = 2
 DEC_DEV_TIMEOUT = 4
+DEC_DEV_BAD_PAGE = 8
+DEC_DEV_NO_PAGES = 16
 DEC_ERR_TOO_LARGE = -10
+DEC_BF16 = 0
+DEC_F32 = 1
+DEC_ROPE_NONE = 0
+DEC_ROPE_LINEAR = 1
+DEC_ROPE_NTK = 2
+DEC_ROPE_PARTS = 3
 LW_ORDER = ("in_norm", "q", "k", "v", "q_norm", "k_norm", "o", "post_norm", "gate", "up", "down")
 
 #: every symbol include/dec.h declares
@@ -29,6 +38,10 @@ EXPORTS = (
     "dec_attention_workspace_bytes", "dec_attention", "dec_kv_quantize_e4m3",
     "dec_attention_noalloc", "dec_verify", "dec_accept_greedy", "dec_generate",
     "dec_init_int8", "dec_quantize_int8", "dec_init_fp8w", "dec_quantize_fp8w",
+    "dec_rope_phases", "dec_rope_apply", "dec_pages_workspace_bytes", "dec_pages_resize",
+    "dec_pages_fork", "dec_pages_compact", "dec_paged_append",
+    "dec_paged_attention_workspace_bytes", "dec_paged_attention", "dec_beam_workspace_bytes",
+    "dec_beam_select", "dec_kv_reorder", "dec_beam_backtrace",
 )
 #: the projections an int8 handle holds as int8 codes + row scales
 PROJ_KEYS = ("q", "k", "v", "o", "gate", "up", "down")
@@ -58,6 +71,35 @@ class dec_kv(ctypes.Structure):
                 ("max_ctx", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
+class dec_rope(ctypes.Structure):
+    _fields_ = [("phases", ctypes.c_void_p), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("mscale", ctypes.c_float)]
+
+
+class dec_pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_layers", ctypes.c_int),
+                ("n_pages", ctypes.c_int), ("page_rows", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("layer_stride", ctypes.c_longlong),
+                ("page_stride", ctypes.c_longlong)]
+
+
+class dec_page_map(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("rows", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int), ("width", ctypes.c_int)]
+
+
+class dec_append(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int), ("dtype", ctypes.c_int), ("n_q_heads", ctypes.c_int),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong),
+                ("v_stride", ctypes.c_longlong), ("q_out", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("seqs", ctypes.c_void_p),
+                ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("rope", ctypes.POINTER(dec_rope))]
+
+
 class DecError(RuntimeError):
     def __init__(self, code: int, what: str):
         self.code = code
@@ -77,6 +119,9 @@ def lib() -> ctypes.CDLL:
                               "`python -m decoder_greedy_decode_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
         P, I, Z, U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_ulonglong
+        S, F = ctypes.c_longlong, ctypes.c_double
+        PG, PM = ctypes.POINTER(dec_pages), ctypes.POINTER(dec_page_map)
+        RP, AP = ctypes.POINTER(dec_rope), ctypes.POINTER(dec_append)
         sig = {
             "dec_init": ([ctypes.POINTER(dec_shape), ctypes.POINTER(dec_weights), ctypes.POINTER(P)], I),
             "dec_free": ([P], None),
@@ -105,6 +150,19 @@ def lib() -> ctypes.CDLL:
             "dec_init_fp8w": ([ctypes.POINTER(dec_shape), ctypes.POINTER(dec_weights_int8),
                                ctypes.POINTER(P)], I),
             "dec_quantize_fp8w": ([P, I, I, P, P, P], I),
+            "dec_rope_phases": ([I, F, I, F, F, F, F, P], I),
+            "dec_rope_apply": ([I, I, I, I, P, S, P, S, P, RP, P], I),
+            "dec_pages_workspace_bytes": ([PG, PM], Z),
+            "dec_pages_resize": ([PG, PM, P, P, Z, P, P], I),
+            "dec_pages_fork": ([PG, PM, P, P, P], I),
+            "dec_pages_compact": ([PG, PM, P, P, Z, P, P], I),
+            "dec_paged_append": ([PG, PM, I, AP, P, P], I),
+            "dec_paged_attention_workspace_bytes": ([PG, I, I], Z),
+            "dec_paged_attention": ([PG, PM, I, I, I, P, S, P, I, P, P, P, Z, P, P], I),
+            "dec_beam_workspace_bytes": ([I, I, I, I], Z),
+            "dec_beam_select": ([I, I, I, I, I, P, S, P, P, I, P, P, P, P, P, Z, P], I),
+            "dec_kv_reorder": ([I, I, I, I, I, I, P, P, I, P, P, P, P], I),
+            "dec_beam_backtrace": ([I, I, I, P, P, P, P], I),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -134,6 +192,58 @@ def _stream(stream) -> Optional[int]:
         import torch
         return int(torch.cuda.current_stream().cuda_stream)
     return int(getattr(stream, "cuda_stream", stream))
+
+
+# --------------------------------------------- checks of the tensor wrappers
+def check_tensor(t, name: str, dtype, shape=None, device=None) -> None:
+    """`t` is a contiguous CUDA tensor of this type, shape and device."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be on {device or 'a CUDA device'}, got {t.device}")
+
+
+def same_device(device, **tensors) -> None:
+    if device.type != "cuda":
+        raise ValueError(f"a CUDA device is needed, got {device}")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def dtype_code(t, name: str) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return DEC_BF16
+    if t.dtype == torch.float32:
+        return DEC_F32
+    raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+_no_guard = contextlib.nullcontext()
+
+
+def on_device(device):
+    """A guard that makes `device` current (calls run on its current stream)."""
+    import torch
+    if device.index is None or torch.cuda.current_device() == device.index:
+        return _no_guard
+    return torch.cuda.device(device)
+
+
+def on_stream(stream, device):
+    """A guard that makes `stream` current (None: as it is), so that scratch
+    allocated within belongs to the stream that uses it."""
+    import torch
+    if stream is None:
+        return _no_guard
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+    return torch.cuda.stream(stream)
 
 
 # ------------------------------------------------------------------ C ABI
@@ -282,3 +392,86 @@ def dec_attention_noalloc(batch: int, n_q_heads: int, n_kv_heads: int, head_dim:
     _ok(lib().dec_attention_noalloc(batch, n_q_heads, n_kv_heads, head_dim, _ptr(q), _ptr(k_cache),
                                     _ptr(v_cache), max_len, _ptr(lengths), _ptr(out), _ptr(status),
                                     _stream(stream)), "dec_attention_noalloc")
+
+
+def dec_rope_phases(rot_dim: int, theta: float, scaling: int, factor: float, orig_ctx: float,
+                    alpha: float, beta: float, phases_host) -> None:
+    _ok(lib().dec_rope_phases(rot_dim, theta, scaling, factor, orig_ctx, alpha, beta,
+                              ctypes.cast(phases_host, ctypes.c_void_p)), "dec_rope_phases")
+
+
+def dec_rope_apply(n_tokens: int, n_heads: int, head_dim: int, dtype: int, x, x_stride: int, out,
+                   out_stride: int, positions, rope: dec_rope, stream=None) -> None:
+    _ok(lib().dec_rope_apply(n_tokens, n_heads, head_dim, dtype, _ptr(x), x_stride, _ptr(out),
+                             out_stride, _ptr(positions), ctypes.byref(rope), _stream(stream)),
+        "dec_rope_apply")
+
+
+def dec_pages_workspace_bytes(pool: dec_pages, pmap: dec_page_map) -> int:
+    return int(lib().dec_pages_workspace_bytes(ctypes.byref(pool), ctypes.byref(pmap)))
+
+
+def dec_pages_resize(pool: dec_pages, pmap: dec_page_map, new_rows, workspace,
+                     workspace_bytes: int, status=None, stream=None) -> None:
+    _ok(lib().dec_pages_resize(ctypes.byref(pool), ctypes.byref(pmap), _ptr(new_rows),
+                               _ptr(workspace), workspace_bytes, _ptr(status), _stream(stream)),
+        "dec_pages_resize")
+
+
+def dec_pages_fork(pool: dec_pages, pmap: dec_page_map, parents, status=None,
+                   stream=None) -> None:
+    _ok(lib().dec_pages_fork(ctypes.byref(pool), ctypes.byref(pmap), _ptr(parents), _ptr(status),
+                             _stream(stream)), "dec_pages_fork")
+
+
+def dec_pages_compact(pool: dec_pages, pmap: dec_page_map, n_live, workspace,
+                      workspace_bytes: int, status=None, stream=None) -> None:
+    _ok(lib().dec_pages_compact(ctypes.byref(pool), ctypes.byref(pmap), _ptr(n_live),
+                                _ptr(workspace), workspace_bytes, _ptr(status), _stream(stream)),
+        "dec_pages_compact")
+
+
+def dec_paged_append(pool: dec_pages, pmap: dec_page_map, layer: int, io: dec_append, status=None,
+                     stream=None) -> None:
+    _ok(lib().dec_paged_append(ctypes.byref(pool), ctypes.byref(pmap), layer, ctypes.byref(io),
+                               _ptr(status), _stream(stream)), "dec_paged_append")
+
+
+def dec_paged_attention_workspace_bytes(pool: dec_pages, batch: int, n_q_heads: int) -> int:
+    return int(lib().dec_paged_attention_workspace_bytes(ctypes.byref(pool), batch, n_q_heads))
+
+
+def dec_paged_attention(pool: dec_pages, pmap: dec_page_map, layer: int, batch: int,
+                        n_q_heads: int, q, q_stride: int, rows, window: int, out, lse, workspace,
+                        workspace_bytes: int, status=None, stream=None) -> None:
+    _ok(lib().dec_paged_attention(ctypes.byref(pool), ctypes.byref(pmap), layer, batch, n_q_heads,
+                                  _ptr(q), q_stride, _ptr(rows), window, _ptr(out), _ptr(lse),
+                                  _ptr(workspace), workspace_bytes, _ptr(status),
+                                  _stream(stream)), "dec_paged_attention")
+
+
+def dec_beam_workspace_bytes(groups: int, beams: int, vocab: int, k: int) -> int:
+    return int(lib().dec_beam_workspace_bytes(groups, beams, vocab, k))
+
+
+def dec_beam_select(groups: int, beams: int, vocab: int, k: int, dtype: int, logits,
+                    row_stride: int, scores, done, eos: int, out_scores, out_parents, out_tokens,
+                    out_done, workspace, workspace_bytes: int, stream=None) -> None:
+    _ok(lib().dec_beam_select(groups, beams, vocab, k, dtype, _ptr(logits), row_stride,
+                              _ptr(scores), _ptr(done), eos, _ptr(out_scores), _ptr(out_parents),
+                              _ptr(out_tokens), _ptr(out_done), _ptr(workspace), workspace_bytes,
+                              _stream(stream)), "dec_beam_select")
+
+
+def dec_kv_reorder(n_layers: int, n_kv_heads: int, head_dim: int, dtype: int, kv_batch: int,
+                   max_ctx: int, values, scales, batch: int, parents, rows, status=None,
+                   stream=None) -> None:
+    _ok(lib().dec_kv_reorder(n_layers, n_kv_heads, head_dim, dtype, kv_batch, max_ctx,
+                             _ptr(values), _ptr(scales), batch, _ptr(parents), _ptr(rows),
+                             _ptr(status), _stream(stream)), "dec_kv_reorder")
+
+
+def dec_beam_backtrace(n_steps: int, groups: int, beams: int, parents, tokens, out,
+                       stream=None) -> None:
+    _ok(lib().dec_beam_backtrace(n_steps, groups, beams, _ptr(parents), _ptr(tokens), _ptr(out),
+                                 _stream(stream)), "dec_beam_backtrace")

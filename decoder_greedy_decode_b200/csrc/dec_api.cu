@@ -687,17 +687,23 @@ extern "C" const char* dec_error_string(int code) {
     default: break;
   }
   if (code > 0) {
-    static thread_local char buf[96];
+    static thread_local char buf[224];
     buf[0] = 0;
     if (code & DEC_DEV_BAD_POSITION) strcat(buf, "device: position out of range; ");
     if (code & DEC_DEV_BAD_TOKEN) strcat(buf, "device: token out of range; ");
     if (code & DEC_DEV_TIMEOUT) strcat(buf, "device: bounded wait ran out; ");
+    if (code & DEC_DEV_BAD_PAGE) strcat(buf, "device: page, sequence or parent out of range; ");
+    if (code & DEC_DEV_NO_PAGES) strcat(buf, "device: too few free pages; ");
     return buf;
   }
   return "unknown status";
 }
 
 extern "C" int dec_last_cuda_error(void) { return g_last_cuda; }
+
+namespace dec {
+int cuda_failed(cudaError_t e) { return cuda_fail(e); }
+}  // namespace dec
 
 // ------------------------------------------------------------ attention
 extern "C" size_t dec_attention_workspace_bytes(int batch, int n_q_heads, int n_kv_heads,

@@ -1,0 +1,549 @@
+// dec_beam.cu -- beam search: the k best continuations of every group of
+// beams, the contiguous cache that follows them, and the chosen sequences.
+//
+// Selection.  score(w, t) = s_w + x_wt - log sum_t exp(x_wt).  Within a row
+// the order of the scores is the order of the logits, so one pass over the
+// logits finds both what the row's sum needs and the only k candidates it can
+// send: a CTA holds a chunk of a row in registers (all its loads in flight at
+// once: the bound is HBM), reduces (max, sum exp) and picks its k largest.
+// A second, dependent launch joins the chunks of each row, and the rows of
+// each group, in fp64.
+//
+// The k largest of a chunk.  Keys (order of the logit, then the lower index)
+// are unique 64-bit words.  The k-th largest of the 64 maxima of groups of
+// four threads is a lower bound of the chunk's k-th largest key; only the k
+// groups that reach it look at their elements again, so at most 4 k x
+// (elements per thread) keys are gathered (a few more than k on random
+// logits), and each finds its place by counting the larger ones.
+#include <cuda_runtime.h>
+
+#include "dec.h"
+#include "dec_paged.h"
+#include "dec_ptx.cuh"
+#include "dec_tc.cuh"
+
+namespace dec {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxK = 32;
+constexpr int kMaxBeams = 32;
+constexpr int kMaxLists = 128;   // chunks of a row
+constexpr int kBig = 32, kSmall = 8;   // logits per thread
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct BeamArgs {
+  int G, W, V, k;
+  const void* logits;
+  long long row_stride;
+  const float* scores;
+  const uint8_t* done;
+  int eos;
+  float* out_scores;
+  int32_t *out_parents, *out_tokens;
+  uint8_t* out_done;
+  int chunks;
+  float2* stat;            // [G W][chunks] (max, sum of exp2((x - max) log2 e))
+  unsigned long long* key; // [G W][chunks][k], descending, 0 = none
+};
+
+__device__ __forceinline__ unsigned long long key_of(float x, uint32_t i) {
+  // (+ 0 makes -0 and 0 one value)
+  return (static_cast<unsigned long long>(order_key(x + 0.f)) << 32) | static_cast<uint32_t>(~i);
+}
+__device__ __forceinline__ float logit_of(unsigned long long key) {
+  const uint32_t u = static_cast<uint32_t>(key >> 32);
+  return __uint_as_float((u & 0x80000000u) ? u & 0x7fffffffu : ~u);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ float one(const float* p) { return *p; }
+  static __device__ __forceinline__ void load(const float* p, float* x) {
+    const float4 v = __ldcs(reinterpret_cast<const float4*>(p));
+    x[0] = v.x;
+    x[1] = v.y;
+    x[2] = v.z;
+    x[3] = v.w;
+  }
+};
+template <>
+struct Vec<uint16_t> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ float one(const uint16_t* p) { return bf16_to_f(*p); }
+  static __device__ __forceinline__ void load(const uint16_t* p, float* x) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = bf16lo(w[i]);
+      x[2 * i + 1] = bf16hi(w[i]);
+    }
+  }
+};
+
+template <typename T, int EPT>
+__global__ void __launch_bounds__(kThreads) rows_kernel(const BeamArgs a) {
+  constexpr int N = Vec<T>::N;
+  constexpr int CHUNK = kThreads * EPT;
+  extern __shared__ unsigned long long s_key[];   // gathered keys [4 k EPT]
+  __shared__ unsigned long long s_max[kThreads / 4];
+  __shared__ unsigned long long s_bound;
+  __shared__ float2 s_stat[kThreads / 32];
+  __shared__ int s_n;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c = blockIdx.x;
+  const long long r = blockIdx.y + static_cast<long long>(blockIdx.z) * gridDim.y;
+  pdl_trigger();
+  if (r >= static_cast<long long>(a.G) * a.W) return;
+  if (a.done && a.done[r]) return;   // its one candidate needs no logits
+  const T* row = static_cast<const T*>(a.logits) + r * a.row_stride;
+  // chunks start on 16-byte boundaries: element i of the row is at i + mis
+  const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+
+  float x[EPT];
+  float m = -INFINITY;
+  int mi = -1;
+  const int base = c * CHUNK - mis;
+#pragma unroll
+  for (int j = 0; j < EPT / N; ++j) {
+    const int i = base + (j * kThreads + tid) * N;
+    if (i >= 0 && i + N <= a.V) {
+      Vec<T>::load(row + i, &x[j * N]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        x[j * N + e] = i + e >= 0 && i + e < a.V ? Vec<T>::one(row + i + e) : -INFINITY;
+    }
+  }
+  if (tid == 0) {
+    s_n = 0;
+    s_bound = 0;
+  }
+  // the thread's largest logit, the first among equals; an element outside
+  // the row is never it unless the thread holds no other
+#pragma unroll
+  for (int j = 0; j < EPT / N; ++j)
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const int i = base + (j * kThreads + tid) * N + e;
+      const bool in = i >= 0 && i < a.V;
+      if (in && (x[j * N + e] > m || (mi < 0 && x[j * N + e] == m))) {
+        m = x[j * N + e];
+        mi = i;
+      }
+    }
+  // (all -inf, or nothing: the sum is 0; a NaN or +inf makes it NaN)
+  const float ref = m == -INFINITY ? 0.f : m;
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < EPT; ++e) s += ex2((x[e] - ref) * kLog2e);
+  float M = warp_max(m);
+  const float Mr = M == -INFINITY ? 0.f : M;
+  s = warp_sum(m == -INFINITY && s == 0.f ? 0.f : s * ex2((ref - Mr) * kLog2e));
+  if (lane == 0) s_stat[warp] = make_float2(M, s);
+
+  const unsigned long long mine = mi < 0 ? 0ull : key_of(m, mi);
+  unsigned long long quad = mine;
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    const unsigned long long other = __shfl_xor_sync(0xffffffffu, quad, o);
+    quad = other > quad ? other : quad;
+  }
+  if ((lane & 3) == 0) s_max[tid >> 2] = quad;
+  __syncthreads();
+  if (tid < kThreads / 4) {
+    const unsigned long long q = s_max[tid];
+    int rank = 0;
+#pragma unroll 16
+    for (int i = 0; i < kThreads / 4; ++i) rank += s_max[i] > q;
+    if (q && rank == a.k - 1) s_bound = q;   // (fewer than k groups hold logits: all are gathered)
+  }
+  __syncthreads();
+  const unsigned long long bound = s_bound;
+  if (mine && mine >= bound) {
+    const float low = logit_of(bound);   // (bound 0: NaN, every comparison below fails)
+#pragma unroll
+    for (int j = 0; j < EPT / N; ++j)
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float v = x[j * N + e];
+        const int i = base + (j * kThreads + tid) * N + e;
+        if (!(v < low) && v == v && i >= 0 && i < a.V) {
+          const unsigned long long key = key_of(v, i);
+          if (key >= bound) s_key[atomicAdd(&s_n, 1)] = key;
+        }
+      }
+  }
+  __syncthreads();
+  const int n = s_n;
+  unsigned long long* out = a.key + (r * a.chunks + c) * a.k;
+  for (int i = tid; i < n; i += kThreads) {
+    const unsigned long long key = s_key[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += s_key[j] > key;
+    if (rank < a.k) out[rank] = key;
+  }
+  if (tid >= n && tid < a.k) out[tid] = 0;
+  if (tid == 0) {
+    float bm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) bm = fmaxf(bm, s_stat[w].x);
+    const float br = bm == -INFINITY ? 0.f : bm;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const float2 t = s_stat[w];
+      sum += t.x == -INFINITY ? t.y : t.y * ex2((t.x - br) * kLog2e);
+    }
+    a.stat[r * a.chunks + c] = make_float2(bm, sum);
+  }
+}
+
+// One CTA per group.  A warp joins a row: its sum, and its k best keys from
+// the chunks' sorted lists (a lane holds the heads of up to four lists).
+__global__ void __launch_bounds__(kThreads) groups_kernel(const BeamArgs a) {
+  __shared__ double s_score[kMaxBeams * kMaxK];
+  __shared__ uint32_t s_at[kMaxBeams * kMaxK];
+  __shared__ bool s_done[kMaxBeams];   // (out_done may be done)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = blockIdx.x;
+  const double ninf = -INFINITY;
+  pdl_wait();
+  for (int w = warp; w < a.W; w += kThreads / 32) {
+    const long long r = static_cast<long long>(g) * a.W + w;
+    const double own = a.scores[r];
+    const bool done = a.done && a.done[r];
+    if (lane == 0) s_done[w] = done;
+    bool flat = !(own > ninf);   // -inf or NaN: no candidate above -inf
+    double lse = 0.0;
+    if (!done && !flat) {
+      float M = -INFINITY;
+      for (int c = lane; c < a.chunks; c += 32) M = fmaxf(M, __ldcg(&a.stat[r * a.chunks + c]).x);
+      M = warp_max(M);
+      double sum = 0.0;
+      for (int c = lane; c < a.chunks; c += 32) {
+        const float2 t = __ldcg(&a.stat[r * a.chunks + c]);
+        sum += static_cast<double>(t.y) *
+               static_cast<double>(t.x == -INFINITY ? 1.f : ex2((t.x - M) * kLog2e));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      lse = static_cast<double>(M) + log(sum);
+      // a NaN or +inf in the row, or nothing but -inf
+      flat = !(M > -INFINITY) || !(M < INFINITY) || !(sum < INFINITY);
+    }
+    double* sc = s_score + w * a.k;
+    uint32_t* at = s_at + w * a.k;
+    const uint32_t row0 = static_cast<uint32_t>(w) * a.V;
+    if (flat || done) {
+      for (int p = lane; p < a.k; p += 32) {
+        if (flat) {
+          sc[p] = ninf;
+          at[p] = row0 + p;
+        } else if (p == 0) {
+          sc[0] = own;
+          at[0] = row0 + a.eos;
+        } else {
+          sc[p] = ninf;
+          at[p] = row0 + (p - 1 < a.eos ? p - 1 : p);
+        }
+      }
+      continue;
+    }
+    const unsigned long long* lists = a.key + r * a.chunks * a.k;
+    unsigned long long head[kMaxLists / 32], then[kMaxLists / 32];
+    int pos[kMaxLists / 32];
+#pragma unroll
+    for (int i = 0; i < kMaxLists / 32; ++i) {
+      const int c = i * 32 + lane;
+      head[i] = c < a.chunks ? __ldcg(lists + c * a.k) : 0ull;
+      then[i] = c < a.chunks && a.k > 1 ? __ldcg(lists + c * a.k + 1) : 0ull;
+      pos[i] = 2;
+    }
+    for (int p = 0; p < a.k; ++p) {
+      unsigned long long best = head[0];
+#pragma unroll
+      for (int i = 1; i < kMaxLists / 32; ++i) best = head[i] > best ? head[i] : best;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const unsigned long long other = __shfl_xor_sync(0xffffffffu, best, o);
+        best = other > best ? other : best;
+      }
+#pragma unroll
+      for (int i = 0; i < kMaxLists / 32; ++i)
+        if (head[i] == best && best) {
+          head[i] = then[i];
+          then[i] = pos[i] < a.k ? __ldcg(lists + (i * 32 + lane) * a.k + pos[i]) : 0ull;
+          ++pos[i];
+        }
+      if (lane == 0) {
+        const double v = own + static_cast<double>(logit_of(best)) - lse;
+        sc[p] = v == v ? v : ninf;
+        at[p] = row0 + static_cast<uint32_t>(~static_cast<uint32_t>(best));
+      }
+    }
+  }
+  __syncthreads();
+  const int n = a.W * a.k;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const double v = s_score[i];
+    const uint32_t at = s_at[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += s_score[j] > v || (s_score[j] == v && s_at[j] < at);
+    if (rank >= a.k) continue;
+    const long long o = static_cast<long long>(g) * a.k + rank;
+    const int w = at / a.V, t = at % a.V;
+    a.out_scores[o] = static_cast<float>(v);
+    a.out_parents[o] = w;
+    a.out_tokens[o] = t;
+    if (a.out_done) a.out_done[o] = s_done[w] || t == a.eos;
+  }
+}
+
+// ------------------------------------------------------- cache reordering
+// A CTA takes the same few rows of one (layer, K or V, head) of every moved
+// sequence: it copies the parents' rows to shared memory, waits, and writes
+// them, so the cache changes in place although parents are themselves moved.
+constexpr int kReThreads = 256;
+constexpr int kRePiece = 1024;   // bytes of a sequence in one CTA
+constexpr int kReBatch = 64;
+
+struct ReorderArgs {
+  uint8_t* kv;
+  float* scales;           // E4M3 caches
+  int B, kv_batch, H, max_ctx, row_bytes, n_rows;  // n_rows of a piece
+  long long planes;        // layers x 2 x heads
+  const int32_t *parents, *rows;
+  int* status;
+};
+
+__global__ void __launch_bounds__(kReThreads) reorder_kernel(const ReorderArgs a) {
+  extern __shared__ __align__(16) uint8_t s_data[];   // [moved][kRePiece], then scales
+  __shared__ int s_to[kReBatch], s_from[kReBatch], s_rows[kReBatch];
+  __shared__ int s_n;
+  const int tid = threadIdx.x;
+  const int r0 = blockIdx.x * a.n_rows;
+  int bad = 0;
+  if (tid < 32) {
+    int n = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int b = b0 + tid;
+      const int p = b < a.B ? a.parents[b] : b, m = b < a.B ? a.rows[b] : 0;
+      if (b < a.B && (p < 0 || p >= a.B)) bad |= DEC_DEV_BAD_PAGE;
+      if (m < 0 || m > a.max_ctx) bad |= DEC_DEV_BAD_POSITION;
+      const bool move = p != b && m > r0;
+      const unsigned mask = __ballot_sync(0xffffffffu, move);
+      if (move) {
+        const int at = n + __popc(mask & ((1u << tid) - 1));
+        s_to[at] = b;
+        s_from[at] = p;
+        s_rows[at] = min(a.n_rows, m - r0);
+      }
+      n += __popc(mask);
+    }
+    if (tid == 0) s_n = n;
+  }
+  if (__syncthreads_or(bad)) {
+    if (bad && blockIdx.x == 0 && blockIdx.y == 0 && a.status) atomicOr(a.status, bad);
+    return;
+  }
+  const int n = s_n;
+  if (n == 0) return;
+  const int pieces = kRePiece / 16;
+  float* s_scale = reinterpret_cast<float*>(s_data + n * kRePiece);
+  for (long long plane = blockIdx.y; plane < a.planes; plane += gridDim.y) {
+    const long long lk = plane / a.H, h = plane % a.H;   // (layer, K or V), head
+    auto row_of = [&](int b) { return ((lk * a.kv_batch + b) * a.H + h) * a.max_ctx + r0; };
+    for (int i = tid; i < n * pieces; i += kReThreads) {
+      const int j = i / pieces, o = (i % pieces) * 16;
+      if (o < s_rows[j] * a.row_bytes)
+        cp_async16_cg(s_data + j * kRePiece + o, a.kv + row_of(s_from[j]) * a.row_bytes + o);
+    }
+    if (a.scales)
+      for (int i = tid; i < n * a.n_rows; i += kReThreads)
+        if (i % a.n_rows < s_rows[i / a.n_rows])
+          s_scale[i] = a.scales[row_of(s_from[i / a.n_rows]) + i % a.n_rows];
+    cp_async_wait_all();
+    __syncthreads();
+    for (int i = tid; i < n * pieces; i += kReThreads) {
+      const int j = i / pieces, o = (i % pieces) * 16;
+      if (o < s_rows[j] * a.row_bytes)
+        *reinterpret_cast<uint4*>(a.kv + row_of(s_to[j]) * a.row_bytes + o) =
+            *reinterpret_cast<const uint4*>(s_data + j * kRePiece + o);
+    }
+    if (a.scales)
+      for (int i = tid; i < n * a.n_rows; i += kReThreads)
+        if (i % a.n_rows < s_rows[i / a.n_rows])
+          a.scales[row_of(s_to[i / a.n_rows]) + i % a.n_rows] = s_scale[i];
+    __syncthreads();
+  }
+}
+
+__global__ void backtrace_kernel(int n, int G, int W, const int32_t* parents,
+                                 const int32_t* tokens, int32_t* out) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= G * W) return;
+  const int g = i / W;
+  int w = i % W;
+  int32_t* o = out + static_cast<long long>(i) * n;
+  for (int t = n - 1; t >= 0; --t) {
+    if (w < 0 || w >= W) {
+      o[t] = -1;
+      continue;
+    }
+    const long long e = (static_cast<long long>(t) * G + g) * W + w;
+    o[t] = tokens[e];
+    w = parents[e];
+  }
+}
+
+struct Plan {
+  int ept, chunks;
+  size_t stat, total;
+};
+// Chunks of 2048 logits while they fill no more than one wave of CTAs (8 to
+// an SM): then latency counts, and more CTAs share a row.  Else 8192.
+Plan plan_of(int rows, int V, int k, int sms) {
+  Plan p{};
+  const int per = 8 - 1;   // most elements before the first 16-byte boundary
+  const long long small = (V + per + kThreads * kSmall - 1) / (kThreads * kSmall);
+  p.ept = small <= kMaxLists && small * rows <= 8ll * sms ? kSmall : kBig;
+  p.chunks = (V + per + kThreads * p.ept - 1) / (kThreads * p.ept);
+  p.stat = round256(sizeof(float2) * static_cast<size_t>(rows) * p.chunks);
+  p.total = p.stat + round256(sizeof(unsigned long long) * static_cast<size_t>(rows) * p.chunks * k);
+  return p;
+}
+
+bool bad_beams(int groups, int beams, int vocab, int k) {
+  return groups < 1 || groups > 65535 || beams < 1 || beams > kMaxBeams || k < 1 || k > kMaxK ||
+         vocab < k || vocab > 1000000;
+}
+
+template <typename T, int EPT>
+cudaError_t launch_beam_rows(const BeamArgs& a, cudaStream_t s) {
+  const size_t smem = sizeof(unsigned long long) * 4 * a.k * EPT;
+  const int rows = a.G * a.W;
+  const int y = rows < 32768 ? rows : 32768;
+  rows_kernel<T, EPT><<<dim3(a.chunks, y, (rows + y - 1) / y), kThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace dec
+
+using namespace dec;
+
+extern "C" size_t dec_beam_workspace_bytes(int groups, int beams, int vocab, int k) {
+  if (bad_beams(groups, beams, vocab, k)) return 0;
+  const int sms = device_sms();
+  return plan_of(groups * beams, vocab, k, sms > 0 ? sms : 148).total;
+}
+
+extern "C" int dec_beam_select(int groups, int beams, int vocab, int k, int dtype,
+                               const void* logits, long long row_stride, const float* scores,
+                               const uint8_t* done, int eos, float* out_scores,
+                               int32_t* out_parents, int32_t* out_tokens, uint8_t* out_done,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (!logits || !scores || !out_scores || !out_parents || !out_tokens || !workspace)
+    return DEC_ERR_NULL;
+  if (bad_beams(groups, beams, vocab, k)) return DEC_ERR_ARG;
+  if (dtype != DEC_BF16 && dtype != DEC_F32) return DEC_ERR_DTYPE;
+  if (eos < -1 || eos >= vocab || (done && eos < 0)) return DEC_ERR_ARG;
+  if (groups * beams > 1 && row_stride < vocab) return DEC_ERR_SHAPE;
+  if (!is_aligned(logits, dtype == DEC_BF16 ? 2 : 4) || !is_aligned(workspace, 256) ||
+      !is_aligned(scores, 4) || !is_aligned(out_scores, 4) || !is_aligned(out_parents, 4) ||
+      !is_aligned(out_tokens, 4))
+    return DEC_ERR_ALIGN;
+  if (k != beams && (out_scores == scores || (out_done && out_done == done))) return DEC_ERR_ARG;
+  const int sms = device_sms();
+  const Plan p = plan_of(groups * beams, vocab, k, sms > 0 ? sms : 148);
+  if (workspace_bytes < p.total) return DEC_ERR_KV_SIZE;
+  if (sms < 0) return sms;
+  BeamArgs a{};
+  a.G = groups;
+  a.W = beams;
+  a.V = vocab;
+  a.k = k;
+  a.logits = logits;
+  a.row_stride = row_stride;
+  a.scores = scores;
+  a.done = done;
+  a.eos = eos;
+  a.out_scores = out_scores;
+  a.out_parents = out_parents;
+  a.out_tokens = out_tokens;
+  a.out_done = out_done;
+  a.chunks = p.chunks;
+  a.stat = static_cast<float2*>(workspace);
+  a.key = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + p.stat);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dtype == DEC_BF16)
+    e = p.ept == kSmall ? launch_beam_rows<uint16_t, kSmall>(a, s)
+                        : launch_beam_rows<uint16_t, kBig>(a, s);
+  else
+    e = p.ept == kSmall ? launch_beam_rows<float, kSmall>(a, s) : launch_beam_rows<float, kBig>(a, s);
+  if (e == cudaSuccess) e = launch_dependent(groups_kernel, dim3(groups), dim3(kThreads), 0, s, a);
+  return e == cudaSuccess ? DEC_OK : cuda_failed(e);
+}
+
+extern "C" int dec_kv_reorder(int n_layers, int n_kv_heads, int head_dim, int dtype, int kv_batch,
+                              int max_ctx, void* values, float* scales, int batch,
+                              const int32_t* parents, const int32_t* rows, int* status,
+                              void* stream) {
+  if (!values || !parents || !rows) return DEC_ERR_NULL;
+  if (n_layers < 1 || n_kv_heads < 1 || (head_dim != 64 && head_dim != 128)) return DEC_ERR_SHAPE;
+  if (dtype != DEC_KV_BF16 && dtype != DEC_KV_FP8_E4M3) return DEC_ERR_DTYPE;
+  const bool fp8 = dtype == DEC_KV_FP8_E4M3;
+  if (fp8 && !scales) return DEC_ERR_NULL;
+  if (batch < 1 || batch > kReBatch || batch > kv_batch) return DEC_ERR_BATCH;
+  if (max_ctx < 16 || max_ctx % 16) return DEC_ERR_ARG;
+  if (!is_aligned(values, 16) || (fp8 && !is_aligned(scales, 4)) || !is_aligned(parents, 4) ||
+      !is_aligned(rows, 4))
+    return DEC_ERR_ALIGN;
+  ReorderArgs a{};
+  a.kv = static_cast<uint8_t*>(values);
+  a.scales = fp8 ? scales : nullptr;
+  a.B = batch;
+  a.kv_batch = kv_batch;
+  a.H = n_kv_heads;
+  a.max_ctx = max_ctx;
+  a.row_bytes = head_dim * (fp8 ? 1 : 2);
+  a.n_rows = kRePiece / a.row_bytes;
+  a.planes = 2ll * n_layers * n_kv_heads;
+  a.parents = parents;
+  a.rows = rows;
+  a.status = status;
+  const int smem = batch * (kRePiece + (fp8 ? a.n_rows * 4 : 0));
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(reorder_kernel, kReBatch * (kRePiece + 64), allowed);
+  if (e != cudaSuccess) return cuda_failed(e);
+  const unsigned x = static_cast<unsigned>((max_ctx + a.n_rows - 1) / a.n_rows);
+  const unsigned y = static_cast<unsigned>(a.planes < 65535 ? a.planes : 65535);
+  reorder_kernel<<<dim3(x, y), kReThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? DEC_OK : cuda_failed(e);
+}
+
+extern "C" int dec_beam_backtrace(int n_steps, int groups, int beams, const int32_t* parents,
+                                  const int32_t* tokens, int32_t* out, void* stream) {
+  if (n_steps < 0 || groups < 1 || beams < 1 || static_cast<long long>(groups) * beams > (1 << 24))
+    return DEC_ERR_ARG;
+  if (n_steps == 0) return DEC_OK;
+  if (!parents || !tokens || !out) return DEC_ERR_NULL;
+  if (!is_aligned(parents, 4) || !is_aligned(tokens, 4) || !is_aligned(out, 4)) return DEC_ERR_ALIGN;
+  const int n = groups * beams;
+  backtrace_kernel<<<(n + 127) / 128, 128, 0, static_cast<cudaStream_t>(stream)>>>(
+      n_steps, groups, beams, parents, tokens, out);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? DEC_OK : cuda_failed(e);
+}

@@ -9,7 +9,7 @@ from typing import Dict, Optional
 
 import torch
 
-from . import capi
+from . import beam, capi
 from .synth import LAYER_KEYS, ModelShape
 
 assert tuple(LAYER_KEYS) == tuple(capi.LW_ORDER)
@@ -84,6 +84,14 @@ class KVCache:
             self.scales = self.buf[off:off + 4 * n // s.head_dim].view(torch.float32).view(shp[:-1])
 
 
+    def reorder(self, parents, rows, status=None, stream=None) -> None:
+        """Sequence b becomes a copy of the first rows[b] rows of sequence
+        parents[b] (int32, the first len(parents) sequences of the cache), in
+        place and all at once."""
+        beam.kv_reorder(self.codes if self.values is None else self.values, parents, rows,
+                        scales=self.scales, status=status, stream=stream)
+
+
 class Decoder:
     """Owns one dec_handle for a model whose weights live in device tensors."""
 
@@ -134,6 +142,50 @@ class Decoder:
         """out_ids.shape[0] greedy steps on the device; positions advance in place."""
         capi.dec_generate(self.h, int(token_ids.numel()), int(out_ids.shape[0]), token_ids,
                           positions, kv.kv, out_ids, eos, stream)
+
+    def beam_search(self, kv: KVCache, token_ids, positions, n_steps: int, beams: int,
+                    eos: int = -1):
+        """n_steps of beam search for groups of `beams` beams.
+
+        token_ids, positions  int32 [groups]: every group's current token and
+                              the row it is written to; sequence g * beams of
+                              `kv` holds the group's rows 0 .. positions[g]-1
+                              (the other beams' sequences are overwritten)
+        Returns (sequences int32 [groups, beams, n_steps], scores fp32 [groups,
+        beams], the sums of log probabilities), best first.  A beam that emits
+        eos is finished: it keeps its score and repeats eos.  Sequence
+        g * beams + w of `kv` ends with the rows of beam w.  Errors found on
+        the device as in step (check)."""
+        G, W, V = int(token_ids.numel()), beams, self.shape.vocab
+        dev = kv.buf.device
+        capi.check_tensor(token_ids, "token_ids", torch.int32, (G,), dev)
+        capi.check_tensor(positions, "positions", torch.int32, (G,), dev)
+        if not 1 <= G * W <= min(self.max_batch, kv.batch):
+            raise ValueError(f"{G} groups of {W} beams need a handle and a cache for {G * W} sequences")
+        if n_steps < 1:
+            raise ValueError("n_steps must be at least 1")
+        with capi.on_device(dev):
+            tok = token_ids.repeat_interleave(W)
+            pos = positions.repeat_interleave(W)
+            first = torch.arange(G, dtype=torch.int32, device=dev).repeat_interleave(W) * W
+            kv.reorder(first, pos)
+            scores = torch.full((G, W), float("-inf"), dtype=torch.float32, device=dev)
+            scores[:, 0] = 0.0     # the beams start alike: one of them counts
+            done = torch.zeros((G, W), dtype=torch.uint8, device=dev)
+            ids = torch.empty_like(tok)
+            logits = torch.empty((G * W, V), dtype=torch.float32, device=dev)
+            parents = torch.empty((n_steps, G, W), dtype=torch.int32, device=dev)
+            tokens = torch.empty((n_steps, G, W), dtype=torch.int32, device=dev)
+            for t in range(n_steps):
+                self.step(kv, tok, pos, ids, logits)
+                r = beam.beam_select(logits.view(G, W, V), scores, k=W,
+                                     done=done if eos >= 0 else None, eos=eos, out_scores=scores,
+                                     out_parents=parents[t], out_tokens=tokens[t],
+                                     out_done=done if eos >= 0 else None)
+                pos.add_(1)
+                kv.reorder(r.parents.view(-1) + first, pos)
+                tok = r.tokens.view(-1)
+            return beam.backtrace(parents, tokens), scores
 
     def verify(self, kv: KVCache, token_ids, positions, seq: int, out_ids, logits=None,
                stream=None) -> None:

@@ -80,7 +80,10 @@ typedef enum dec_status {
    * dec_check(); the step that saw them wrote -1 to every out_ids entry */
   DEC_DEV_BAD_POSITION = 1,   /* a position < 0 or >= max_ctx */
   DEC_DEV_BAD_TOKEN = 2,      /* a token id < 0 or >= vocab */
-  DEC_DEV_TIMEOUT = 4         /* a bounded device wait ran out (see dec_set_timeout_ns) */
+  DEC_DEV_TIMEOUT = 4,        /* a bounded device wait ran out (see dec_set_timeout_ns) */
+  /* raised in the `status` argument of the paged-cache and beam calls */
+  DEC_DEV_BAD_PAGE = 8,       /* a page id, sequence or parent out of range */
+  DEC_DEV_NO_PAGES = 16       /* too few free pages */
 } dec_status;
 
 /* ------------------------------------------------------------------ */
@@ -452,6 +455,260 @@ int dec_quantize_fp8w(const void *w, int rows, int cols, uint8_t *codes, float *
  * [rows, dim], scales fp32 [rows] (all device).  Asynchronous on `stream`. */
 int dec_kv_quantize_e4m3(const float *x, int rows, int dim, uint8_t *codes, float *scales,
                          void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Rotary positions                                                    */
+/* ------------------------------------------------------------------ */
+
+/* Element types of activations passed to the calls below. */
+typedef enum dec_dtype { DEC_BF16 = 0, DEC_F32 = 1 } dec_dtype;
+
+/* How the angles are scaled for contexts longer than the trained one
+ * (factor s, trained length L0; f_i = theta^(-2i/R) for pair i of R/2):
+ *   NONE    f_i
+ *   LINEAR  f_i / s (positions interpolated)
+ *   NTK     (theta * s^(R/(R-2)))^(-2i/R) (the base raised; R > 2)
+ *   PARTS   g_i f_i + (1 - g_i) f_i / s, g_i = clamp((r_i - alpha) /
+ *           (beta - alpha), 0, 1) with r_i = L0 f_i / (2 pi) turns over the
+ *           trained length: fast pairs keep their angle, slow pairs are
+ *           interpolated. */
+typedef enum dec_rope_scaling {
+  DEC_ROPE_NONE = 0,
+  DEC_ROPE_LINEAR = 1,
+  DEC_ROPE_NTK = 2,
+  DEC_ROPE_PARTS = 3
+} dec_rope_scaling;
+
+/* The angle table of a rotation: phases[i] (i < rot_dim/2), the turns that
+ * pair i makes per position as a 64-bit binary fraction (f_i / 2 pi * 2^64,
+ * modulo one turn).  phases is a HOST array here (no GPU work); the calls
+ * below read a device copy of it.  A position times a phase, modulo 2^64, is
+ * the angle to 2^-33 turns at every int32 position.
+ * rot_dim even, 2..128; theta > 1, factor > 0 (NONE ignores it), orig_ctx > 0
+ * and beta > alpha for PARTS (DEC_ERR_ARG). */
+int dec_rope_phases(int rot_dim, double theta, int scaling, double factor, double orig_ctx,
+                    double alpha, double beta, uint64_t *phases);
+
+/* A rotation of the first rot_dim elements of a head; the others pass
+ * through.  Pair i is elements (i, i + rot_dim/2), or (2i, 2i + 1) when
+ * interleaved: (a, b) -> mscale * (a cos - b sin, b cos + a sin). */
+typedef struct dec_rope {
+  const uint64_t *phases;   /* device, [rot_dim/2], 8-byte aligned */
+  int rot_dim;              /* even, 2..head_dim */
+  int interleaved;
+  float mscale;             /* factor of the rotated elements (1 = none) */
+} dec_rope;
+
+/* Rotate the heads of a tensor by their tokens' positions.
+ *   x, out     [n_tokens, n_heads, head_dim] of `dtype`, x_stride /
+ *              out_stride elements between tokens (multiples of 4, at least
+ *              n_heads * head_dim when n_tokens > 1; heads contiguous);
+ *              out may be x (same stride); otherwise they do not overlap
+ *   positions  int32 [n_tokens] (device); the row of a token whose position
+ *              is negative (padding) is copied as it is
+ * The angle is exact to 2^-33 turns at any position, the rotation is fp32,
+ * rounded once to `dtype`.  head_dim 64 or 128 (DEC_ERR_SHAPE); x and out
+ * 4-element aligned (DEC_ERR_ALIGN).  Asynchronous on `stream`. */
+int dec_rope_apply(int n_tokens, int n_heads, int head_dim, int dtype, const void *x,
+                   long long x_stride, void *out, long long out_stride,
+                   const int32_t *positions, const dec_rope *rope, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Paged KV cache                                                      */
+/* ------------------------------------------------------------------ */
+
+/* A pool of cache pages in caller buffers.  A page holds page_rows rows of
+ * every KV head; row r of head h of page p of layer l starts at element
+ *   l * layer_stride + p * page_stride + (h * page_rows + r) * head_dim
+ * of k and v (bf16 values, or E4M3 codes of one byte), and its fp32 scale at
+ * that element / head_dim of k_scale / v_scale (E4M3 pools only; scales are
+ * positive, as dec_kv_quantize_e4m3 writes them).  The rows of different
+ * layers and pages do not overlap (layers and pages may be nested either
+ * way, and K and V may share one buffer). */
+typedef struct dec_pages {
+  void *k, *v;                 /* device, 16-byte aligned */
+  float *k_scale, *v_scale;    /* device; NULL for bf16 */
+  int n_layers;
+  int n_pages;
+  int page_rows;               /* a power of two, 8..1024 */
+  int n_kv_heads;
+  int head_dim;                /* 64 or 128 */
+  int dtype;                   /* dec_kv_dtype */
+  long long layer_stride;      /* elements, multiples of head_dim, at least */
+  long long page_stride;       /* n_kv_heads * page_rows * head_dim */
+} dec_pages;
+
+/* Which pages hold which sequence (device arrays, caller-owned).  Entry j of
+ * a sequence's table row is the page of its rows j * page_rows .. ; entries
+ * behind its last page are -1.  refs counts the table entries that name a
+ * page, over all sequences: 0 = free.  An empty map is table = -1, rows = 0,
+ * refs = 0.  All sequences of one map share the counts of its pool. */
+typedef struct dec_page_map {
+  int32_t *table;   /* [n_seqs][width] */
+  int32_t *rows;    /* [n_seqs] rows that each sequence holds */
+  int32_t *refs;    /* [n_pages] */
+  int n_seqs;       /* 1..4096 */
+  int width;        /* pages per sequence; width * page_rows <= 2^30 */
+} dec_page_map;
+
+/* Device scratch (256-byte aligned, uninitialised) of dec_pages_resize and
+ * dec_pages_compact (0 for an invalid pool or map).  Calls that overlap on
+ * the GPU need separate scratch, and calls on one map must not overlap. */
+size_t dec_pages_workspace_bytes(const dec_pages *pool, const dec_page_map *map);
+
+/* Let every sequence s hold new_rows[s] rows (int32 [n_seqs], device;
+ * negative = leave it as it is): reserve rows before they are appended, crop
+ * after a rejected draft, free with 0.
+ *   - Pages behind the last row of a shrinking sequence are released (a page
+ *     whose count reaches 0 is free for this very call).
+ *   - A growing sequence whose last page is partly filled and shared will
+ *     write into it, so it gets a page of its own with the rows it holds
+ *     copied, in every layer; of the sequences that share the page, the ones
+ *     with lower numbers are copied until one holder is left.
+ *   - New pages are the free pages with the lowest numbers, in the order of
+ *     (sequence, table entry).
+ * If the free pages do not suffice (DEC_DEV_NO_PAGES), a new_rows exceeds
+ * width * page_rows (DEC_DEV_BAD_POSITION) or a page to be released or copied
+ * is out of range (DEC_DEV_BAD_PAGE), the bit is set in *status (device int,
+ * may be NULL) and nothing is changed.  Asynchronous on `stream`. */
+int dec_pages_resize(const dec_pages *pool, const dec_page_map *map, const int32_t *new_rows,
+                     void *workspace, size_t workspace_bytes, int *status, void *stream);
+
+/* All sequences at once become copies of their parents: sequence s holds the
+ * pages and rows that parents[s] (int32 [n_seqs], device) held before the
+ * call; a negative parent empties it.  No data moves: pages are shared, and
+ * dec_pages_resize copies a shared page before it is written.  Pages that no
+ * sequence holds any more are free.  A parent >= n_seqs raises
+ * DEC_DEV_BAD_PAGE and nothing is changed; a table entry outside
+ * [-1, n_pages) raises it and counts as -1.  Asynchronous on `stream`. */
+int dec_pages_fork(const dec_pages *pool, const dec_page_map *map, const int32_t *parents,
+                   int *status, void *stream);
+
+/* Move the live pages (count > 0) with numbers >= n to the free pages below
+ * n, where n is the number of live pages, the i-th such page to the i-th
+ * such free page; tables and counts follow, *n_live (device int32) = n.
+ * Pages n .. n_pages - 1 are then free (a pool can be shrunk to n).  A table
+ * entry out of range raises DEC_DEV_BAD_PAGE and is left as it is.
+ * Asynchronous on `stream`. */
+int dec_pages_compact(const dec_pages *pool, const dec_page_map *map, int32_t *n_live,
+                      void *workspace, size_t workspace_bytes, int *status, void *stream);
+
+/* One call's rows for dec_paged_append.  q, k and v are [n_tokens, heads,
+ * head_dim] of `dtype` with their own element strides between tokens (slices
+ * of one projection's output are fine), 4-element aligned, strides multiples
+ * of 4. */
+typedef struct dec_append {
+  int n_tokens;
+  int dtype;                  /* dec_dtype of q, k and v */
+  int n_q_heads;              /* 0 with q = NULL */
+  const void *q, *k, *v;
+  long long q_stride, k_stride, v_stride;
+  void *q_out;                /* bf16 [n_tokens, n_q_heads, head_dim] */
+  const int32_t *positions;   /* [n_tokens] row each token is written to;
+                               * negative = padding, skipped whole */
+  const int32_t *seqs;        /* [n_tokens] its sequence; NULL: token i is sequence i */
+  const void *q_norm, *k_norm;/* bf16 [head_dim] RMSNorm gains, or NULL for none */
+  float eps;
+  const dec_rope *rope;       /* HOST struct, or NULL for no rotation */
+} dec_append;
+
+/* Store the keys and values of new tokens in the pages of one layer, the keys
+ * (and the queries into q_out) normalised per head and rotated as dec_step
+ * does it before its own append: RMSNorm with the gain where one is given,
+ * then the rotation, in fp32, rounded once to bf16 or quantised per row to
+ * E4M3 exactly as dec_kv_quantize_e4m3 does.  Any mix of sequences and any
+ * number of tokens per sequence (a decode step, prompts, draft blocks); the
+ * pages must have been reserved (dec_pages_resize) and (sequence, position)
+ * pairs must be distinct: a row named twice holds elements of either token.
+ * A token whose sequence is out of range or whose page is not assigned
+ * raises DEC_DEV_BAD_PAGE, a position behind the table's end
+ * DEC_DEV_BAD_POSITION; such a token is skipped whole.  map->rows and
+ * map->refs are not used.  Asynchronous on `stream`. */
+int dec_paged_append(const dec_pages *pool, const dec_page_map *map, int layer,
+                     const dec_append *io, int *status, void *stream);
+
+/* Scratch of dec_paged_attention (256-byte aligned, uninitialised; 0 for an
+ * invalid request).  Calls that overlap on the GPU need separate scratch. */
+size_t dec_paged_attention_workspace_bytes(const dec_pages *pool, int batch, int n_q_heads);
+
+/* dec_attention over a paged cache: one new token per sequence.
+ *   out[b, h, :] = sum_j softmax_j(q[b,h,:] . K[j,:] / sqrt(head_dim)) V[j,:]
+ *   lse[b, h]    = log sum_j exp(q[b,h,:] . K[j,:] / sqrt(head_dim))
+ * over rows j of sequence b, max(0, n - window) <= j < n, n = rows[b].
+ *   batch      sequences 0 .. batch-1 of the map (<= map->n_seqs)
+ *   q          bf16 [batch, n_q_heads, head_dim], q_stride elements between
+ *              sequences (a multiple of 8, 16-byte aligned)
+ *   rows       int32 [batch] (device) or NULL for map->rows; 0 = an empty
+ *              sequence: out 0, lse -inf
+ *   window     0 = all rows; else the last `window` rows (table entries whose
+ *              rows all lie before them are not read and may be -1)
+ *   out        fp32 [batch, n_q_heads, head_dim]
+ *   lse        fp32 [batch, n_q_heads] or NULL
+ * Rows outside the range are not read.  n_q_heads / n_kv_heads <= 8.  The
+ * work is split evenly over the GPU by the lengths on the device, whatever
+ * their mix.  rows[b] < 0 or behind the table's end raises
+ * DEC_DEV_BAD_POSITION, an unassigned page DEC_DEV_BAD_PAGE; that sequence's
+ * outputs (of the KV heads concerned) are left as they were.  map->refs is
+ * not used.  Asynchronous on `stream` (two launches, the second one
+ * dependent). */
+int dec_paged_attention(const dec_pages *pool, const dec_page_map *map, int layer, int batch,
+                        int n_q_heads, const void *q, long long q_stride, const int32_t *rows,
+                        int window, float *out, float *lse, void *workspace,
+                        size_t workspace_bytes, int *status, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Beam search                                                         */
+/* ------------------------------------------------------------------ */
+
+/* Scratch of dec_beam_select (256-byte aligned, uninitialised; 0 for an
+ * invalid request).  Calls that overlap on the GPU need separate scratch. */
+size_t dec_beam_workspace_bytes(int groups, int beams, int vocab, int k);
+
+/* The k best continuations of every group of beams.  Candidate (w, t) of a
+ * group scores scores[w] + logits[w][t] - logsumexp(logits[w]); a beam whose
+ * done flag is set has one candidate, its end token at its own score.  The k
+ * highest are written best first; equal scores go to the lower w * vocab + t.
+ * A score that is not a number counts as -inf (so does every candidate of a
+ * row that holds a NaN or +inf, or nothing but -inf).
+ *   logits       [groups * beams, vocab] of `dtype`, row_stride elements
+ *                between rows (any; element-aligned)
+ *   scores       fp32 [groups, beams]; -inf switches a beam off
+ *   done         uint8 [groups, beams] or NULL
+ *   eos          end token, in [0, vocab), or -1 for none (done = NULL)
+ *   out_scores   fp32 [groups, k]; out_parents int32 [groups, k] (beam within
+ *                the group); out_tokens int32 [groups, k]; out_done uint8
+ *                [groups, k] (done before, or the token is eos), may be NULL.
+ *                With k = beams, out_scores may be scores and out_done done.
+ * beams 1..32, k 1..32, k <= vocab <= 1000000.  Scores are summed and compared in fp64
+ * and rounded once.  Asynchronous on `stream`. */
+int dec_beam_select(int groups, int beams, int vocab, int k, int dtype, const void *logits,
+                    long long row_stride, const float *scores, const uint8_t *done, int eos,
+                    float *out_scores, int32_t *out_parents, int32_t *out_tokens,
+                    uint8_t *out_done, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Sequences 0 .. batch-1 of a contiguous cache (the layout of dec_kv: values
+ * [n_layers][2][kv_batch][n_kv_heads][max_ctx][head_dim], and for an E4M3
+ * cache its scales [n_layers][2][kv_batch][n_kv_heads][max_ctx]) become
+ * copies of their parents, in place and all at once: rows 0 .. rows[b]-1 of
+ * sequence b, in every layer, are those that sequence parents[b] held before
+ * the call; rows behind them are left as they were.
+ *   dtype           dec_kv_dtype; scales is NULL for bf16
+ *   values          16-byte aligned
+ *   parents, rows   int32 [batch] (device); batch <= 64 and <= kv_batch
+ * max_ctx is a multiple of 16.  A parent outside [0, batch) raises
+ * DEC_DEV_BAD_PAGE, rows[b] outside [0, max_ctx] DEC_DEV_BAD_POSITION, in
+ * *status (device int, may be NULL), and nothing is changed.  Asynchronous
+ * on `stream`. */
+int dec_kv_reorder(int n_layers, int n_kv_heads, int head_dim, int dtype, int kv_batch,
+                   int max_ctx, void *values, float *scales, int batch, const int32_t *parents,
+                   const int32_t *rows, int *status, void *stream);
+
+/* The token sequences that a search's choices spell: tokens, parents int32
+ * [n_steps][groups][beams] (parents within the group), out int32 [groups]
+ * [beams][n_steps].  A parent outside [0, beams) writes -1 to the steps
+ * before it.  Asynchronous on `stream`. */
+int dec_beam_backtrace(int n_steps, int groups, int beams, const int32_t *parents,
+                       const int32_t *tokens, int32_t *out, void *stream);
 
 #ifdef __cplusplus
 }
