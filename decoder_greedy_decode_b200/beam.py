@@ -32,6 +32,13 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = N
     apart), scores fp32 [groups, beams], done uint8 [groups, beams] (finished
     beams; needs eos).  k defaults to beams.  With k = beams out_scores may be
     scores and out_done done."""
+    dev = logits.device
+    if dev.type != "cuda":
+        raise ValueError("logits must be on a CUDA device")
+    if capi.elsewhere(dev, stream):
+        with capi.guard(dev, stream):
+            return beam_select(logits, scores, k, done, eos, out_scores, out_parents, out_tokens,
+                               out_done)
     if logits.dim() != 3 or logits.stride(2) != 1:
         raise ValueError("logits must be [groups, beams, vocab] with contiguous rows")
     G, W, V = logits.shape
@@ -40,28 +47,32 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = N
     if G > 1 and W > 1 and logits.stride(0) != W * row:
         raise ValueError("the rows of logits must be equally far apart")
     k = W if k is None else int(k)
-    dev = logits.device
     capi.check_tensor(scores, "scores", torch.float32, (G, W), dev)
     if done is not None:
         capi.check_tensor(done, "done", torch.uint8, (G, W), dev)
-    for name, t, dt in (("out_scores", out_scores, torch.float32),
-                        ("out_parents", out_parents, torch.int32),
-                        ("out_tokens", out_tokens, torch.int32), ("out_done", out_done, torch.uint8)):
-        if t is not None:
-            capi.check_tensor(t, name, dt, (G, k), dev)
-    with capi.on_device(dev), capi.on_stream(stream, dev):
-        nb = capi.dec_beam_workspace_bytes(G, W, V, k)
-        ws = torch.empty(max(nb, 256), dtype=torch.uint8, device=dev)
-        if out_scores is None:
-            out_scores = torch.empty((G, max(k, 0)), dtype=torch.float32, device=dev)
-        if out_parents is None:
-            out_parents = torch.empty((G, max(k, 0)), dtype=torch.int32, device=dev)
-        if out_tokens is None:
-            out_tokens = torch.empty((G, max(k, 0)), dtype=torch.int32, device=dev)
-        if out_done is None and eos >= 0:
-            out_done = torch.empty((G, max(k, 0)), dtype=torch.uint8, device=dev)
-        capi.dec_beam_select(G, W, V, k, capi.dtype_code(logits, "logits"), logits, row, scores,
-                             done, eos, out_scores, out_parents, out_tokens, out_done, ws, nb)
+    nb = capi.lib().dec_beam_workspace_bytes(G, W, V, k)
+    shape = (G, max(k, 0))
+    ws = torch.empty(nb or 256, dtype=torch.uint8, device=dev)
+
+    def result(t, name, dtype):
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        capi.check_tensor(t, name, dtype, shape, dev)
+        return t
+
+    out_scores = result(out_scores, "out_scores", torch.float32)
+    out_parents = result(out_parents, "out_parents", torch.int32)
+    out_tokens = result(out_tokens, "out_tokens", torch.int32)
+    if out_done is not None or eos >= 0:
+        out_done = result(out_done, "out_done", torch.uint8)
+    rc = capi.lib().dec_beam_select(
+        G, W, V, k, capi.dtype_code(logits, "logits"), logits.data_ptr(), row, scores.data_ptr(),
+        None if done is None else done.data_ptr(), eos, out_scores.data_ptr(),
+        out_parents.data_ptr(), out_tokens.data_ptr(),
+        None if out_done is None else out_done.data_ptr(), ws.data_ptr(), nb,
+        capi.current_stream_of(dev))
+    if rc:
+        raise capi.DecError(rc, "dec_beam_select")
     return Selection(out_scores, out_parents, out_tokens, out_done)
 
 
@@ -76,6 +87,11 @@ def kv_reorder(values: torch.Tensor, parents: torch.Tensor, rows: torch.Tensor,
         raise ValueError("values must be [n_layers, 2, batch, n_kv_heads, max_ctx, head_dim]")
     L, _, B, H, ctx, D = values.shape
     dev = values.device
+    if dev.type != "cuda":
+        raise ValueError("values must be on a CUDA device")
+    if capi.elsewhere(dev, stream):
+        with capi.guard(dev, stream):
+            return kv_reorder(values, parents, rows, scales, status)
     if values.dtype == torch.bfloat16 and scales is None:
         code = capi.DEC_KV_BF16
     elif values.dtype == torch.uint8 and scales is not None:
@@ -89,8 +105,12 @@ def kv_reorder(values: torch.Tensor, parents: torch.Tensor, rows: torch.Tensor,
     capi.check_tensor(rows, "rows", torch.int32, (n,), dev)
     if status is not None:
         capi.check_tensor(status, "status", torch.int32, (1,), dev)
-    with capi.on_device(dev), capi.on_stream(stream, dev):
-        capi.dec_kv_reorder(L, H, D, code, B, ctx, values, scales, n, parents, rows, status)
+    rc = capi.lib().dec_kv_reorder(
+        L, H, D, code, B, ctx, values.data_ptr(), None if scales is None else scales.data_ptr(), n,
+        parents.data_ptr(), rows.data_ptr(), None if status is None else status.data_ptr(),
+        capi.current_stream_of(dev))
+    if rc:
+        raise capi.DecError(rc, "dec_kv_reorder")
 
 
 def backtrace(parents: torch.Tensor, tokens: torch.Tensor, stream=None) -> torch.Tensor:
@@ -102,7 +122,9 @@ def backtrace(parents: torch.Tensor, tokens: torch.Tensor, stream=None) -> torch
     capi.check_tensor(parents, "parents", torch.int32, None)
     capi.check_tensor(tokens, "tokens", torch.int32, (n, G, W), parents.device)
     dev = parents.device
-    with capi.on_device(dev), capi.on_stream(stream, dev):
-        out = torch.empty((G, W, n), dtype=torch.int32, device=dev)
-        capi.dec_beam_backtrace(n, G, W, parents, tokens, out)
+    if capi.elsewhere(dev, stream):
+        with capi.guard(dev, stream):
+            return backtrace(parents, tokens)
+    out = torch.empty((G, W, n), dtype=torch.int32, device=dev)
+    capi.dec_beam_backtrace(n, G, W, parents, tokens, out, capi.current_stream_of(dev))
     return out

@@ -197,14 +197,12 @@ def _stream(stream) -> Optional[int]:
 # --------------------------------------------- checks of the tensor wrappers
 def check_tensor(t, name: str, dtype, shape=None, device=None) -> None:
     """`t` is a contiguous CUDA tensor of this type, shape and device."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be on {device or 'a CUDA device'}, got {t.device}")
+    if t.dtype != dtype or (shape is not None and t.shape != shape) or not t.is_contiguous() \
+            or not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be contiguous {dtype}"
+                         + (f" of shape {tuple(shape)}" if shape is not None else "")
+                         + f" on {device or 'a CUDA device'}, got {t.dtype} {tuple(t.shape)} with "
+                         f"strides {t.stride()} on {t.device}")
 
 
 def same_device(device, **tensors) -> None:
@@ -224,26 +222,39 @@ def dtype_code(t, name: str) -> int:
     raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
 
-_no_guard = contextlib.nullcontext()
+class guard:
+    """Makes `device`, and `stream` if it is not None, current: kernels run
+    there and scratch allocated within belongs to that stream."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        import torch
+        self.stack = contextlib.ExitStack()
+        self.stack.enter_context(torch.cuda.device(self.device))
+        if self.stream is not None:
+            s = self.stream
+            if not isinstance(s, torch.cuda.Stream):
+                s = torch.cuda.ExternalStream(int(getattr(s, "cuda_stream", s)), device=self.device)
+            self.stack.enter_context(torch.cuda.stream(s))
+
+    def __exit__(self, *exc):
+        return self.stack.__exit__(*exc)
 
 
-def on_device(device):
-    """A guard that makes `device` current (calls run on its current stream)."""
+def elsewhere(device, stream) -> bool:
+    """Whether a call on `device` and `stream` (None: the current one) needs a
+    guard before it can use current_stream_of()."""
     import torch
-    if device.index is None or torch.cuda.current_device() == device.index:
-        return _no_guard
-    return torch.cuda.device(device)
+    return stream is not None or torch.cuda.current_device() != device.index
 
 
-def on_stream(stream, device):
-    """A guard that makes `stream` current (None: as it is), so that scratch
-    allocated within belongs to the stream that uses it."""
+def current_stream_of(device) -> int:
+    """The raw current stream of `device`."""
     import torch
-    if stream is None:
-        return _no_guard
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
-    return torch.cuda.stream(stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # 2 us less than a Stream object
+    return raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream
 
 
 # ------------------------------------------------------------------ C ABI

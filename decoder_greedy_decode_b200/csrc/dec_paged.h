@@ -33,7 +33,7 @@ inline int check_pool(const dec_pages* p) {
   if (p->dtype != DEC_KV_BF16 && p->dtype != DEC_KV_FP8_E4M3) return DEC_ERR_DTYPE;
   if (p->dtype == DEC_KV_FP8_E4M3 && (!p->k_scale || !p->v_scale)) return DEC_ERR_NULL;
   if (p->head_dim != 64 && p->head_dim != 128) return DEC_ERR_SHAPE;
-  if (p->n_layers < 1 || p->n_kv_heads < 1 || p->n_kv_heads > 4096 || p->n_pages < 1)
+  if (p->n_layers < 1 || p->n_kv_heads < 1 || p->n_kv_heads > 256 || p->n_pages < 1)
     return DEC_ERR_SHAPE;
   if (p->page_rows < 8 || p->page_rows > 1024 || (p->page_rows & (p->page_rows - 1)))
     return DEC_ERR_SHAPE;
@@ -42,7 +42,9 @@ inline int check_pool(const dec_pages* p) {
       p->page_stride % p->head_dim)
     return DEC_ERR_SHAPE;
   if (!is_aligned(p->k, 16) || !is_aligned(p->v, 16)) return DEC_ERR_ALIGN;
-  if (p->dtype == DEC_KV_FP8_E4M3 && (!is_aligned(p->k_scale, 4) || !is_aligned(p->v_scale, 4)))
+  if (p->dtype == DEC_KV_FP8_E4M3 &&
+      (!is_aligned(p->k_scale, 16) || !is_aligned(p->v_scale, 16) ||
+       p->layer_stride % (4 * p->head_dim) || p->page_stride % (4 * p->head_dim)))
     return DEC_ERR_ALIGN;
   return DEC_OK;
 }

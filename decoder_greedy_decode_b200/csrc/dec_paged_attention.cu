@@ -9,35 +9,41 @@
 //
 // Bound and split.  Every K and V row is read once and used for the query
 // heads of its KV head only: the bound is HBM.  The unit of work is a tile of
-// 16 rows of one (sequence, KV head).  The tiles of all sequences, counted
-// from the lengths on the device, are dealt in equal contiguous runs to the
-// warps of a grid that just fills the GPU, so a ragged batch costs what its
-// rows cost.  A warp works alone: it copies its tiles into a ring of its own
-// (cp.async, several tiles ahead, across sequence boundaries), so no barrier
-// holds the stream up.  A run that covers a whole (sequence, KV head) writes
-// the output; otherwise it leaves its state in the workspace and a second,
-// dependent launch joins the states in run order (the result does not depend
-// on timing).
+// 16 or 32 rows of one sequence.  The tiles of all sequences, counted from the
+// lengths on the device, are dealt in equal contiguous runs to groups of
+// warps of a grid that just fills the GPU, one warp of a group per KV head
+// (neighbouring warps read neighbouring parts of the same pages), so a ragged
+// batch costs what its rows cost.  A warp works alone: one lane copies its
+// tiles into a ring of the warp's own, several ahead and across sequence
+// boundaries, so no CTA barrier holds the stream up.  A run that covers a
+// whole sequence writes its output; otherwise it leaves its state in the
+// workspace and a second, dependent launch joins the states in run order (the
+// result does not depend on timing).  TMA does the copies: loads alone
+// (nothing computed) ran at 7.0 TB/s so, and at 5.2 TB/s with per-lane
+// cp.async of the same rings (32 sequences of 16K to 32K rows).
 //
-// Tile layout.  Every lane copies exactly the 16-byte pieces that it will use
-// itself, into its own column of the ring ([piece][lane], free of bank
-// conflicts), so a tile needs no barrier either.  For the scores the rows
-// are the M of a 16x8x16 warp MMA and the heads its N; the order of the head
-// elements along K is free as long as q uses the same, so a lane's 16-byte
-// piece of a K row is its A fragment as it stands.  For the output, V^T is A
-// (M = head elements, K = rows): the lane holds four rows of the same
-// elements and one byte permute per register pairs two rows.  P goes from the
-// score layout to the B fragment by a warp-wide 8x8 transpose.
+// Tile layout.  For the scores the rows are the M of a 16x8x16 warp MMA and
+// the heads its N.  The order of the head elements along K is free as long as
+// q uses the same, so a lane's 16-byte piece of a K row is its A fragment as
+// it stands.  For the output, V^T is A (M = head elements, K = rows): the lane
+// reads the same 16 bytes of four rows and one byte permute per register pairs
+// two rows.  P goes from the score layout to the B fragment by a warp-wide 8x8
+// transpose.  Rows of 128 bytes are swizzled by TMA (16-byte piece c of row r
+// sits at c ^ (r mod 8)), and M index i of an octet of rows is row
+// i ^ (i odd ? 4 : 0): with both, the K reads (two rows, four pieces) and the
+// V reads (four rows, two pieces) of a quarter warp hit 32 different banks.
 //
-// Rounding.  P enters the second MMA as two bf16 planes, hi = bf16(p) and
-// lo = bf16(p - hi) (2^-17 relative; one plane would cost 2^-8).  lo may be 0
-// or negative, so it meets V with infinities made finite: hi alone decides
-// what an infinite element gives.  E4M3 codes
+// Rounding.  P enters the second MMA as three bf16 planes, its 24 bits cut
+// into 8 each: exact (one rounded plane would cost 2^-8, two 2^-17).  A
+// tile's sums start from zero and are added to the running
+// ones in fp32: the tensor core cuts, and a chain of thousands of tiles into
+// one accumulator would drift (1.2e-5 of the output at 24K rows).  E4M3 codes
 // are exact in f16 and stay codes: the K scale multiplies the score, the V
 // scale multiplies p, whose planes are then f16 after a power-of-two factor F
 // per head that keeps the largest p * scale near 2^14 (2^-22 relative, values
 // below 2^-39 of the largest lost).  q is made f16 by a power of two per
 // head, exact down to 2^-38 of the head's largest element.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "dec.h"
@@ -50,9 +56,11 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 16;     // rows of a tile
 constexpr int kMaxHeads = 8;  // query heads per KV head (the N of the MMA)
 
+#ifndef KCF
+#define KCF(D, FP8) ((FP8) ? 3 : (D) == 128 ? 2 : 3)
+#endif
 struct PagedArgs {
   PoolView pool;
   const int32_t* table;
@@ -65,25 +73,28 @@ struct PagedArgs {
   float* out;
   float* lse;
   float* part;     // [warps][2] states: rep x D sums, then rep x (m, l)
-  int2* desc;      // [B][Hkv] (first warp, warps) of the states to join
+  int2* desc;      // [B] (first worker, workers) whose states are joined
   int* status;
 };
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// c += a b; with FIRST, c = a b.
+template <bool F16, bool FIRST = false>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  const float z0 = FIRST ? 0.f : c[0], z1 = FIRST ? 0.f : c[1], z2 = FIRST ? 0.f : c[2],
+              z3 = FIRST ? 0.f : c[3];
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z0), "f"(z1), "f"(z2), "f"(z3));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z0), "f"(z1), "f"(z2), "f"(z3));
 }
 // The transpose of an 8x8 matrix of 16-bit values spread over the warp (lane
 // l holds row l/4, columns 2(l%4) and the next).
@@ -92,22 +103,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-// BYTES (4, 8 or 16) global -> shared; zeros when !valid (src is not read).
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? BYTES : 0;
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES),
-                 "r"(n)
-                 : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Box at (element x, row y, page z) of a pool's tensor map.  x is 0 or 64
+// elements of bf16 or 0 of E4M3: a multiple of 16 bytes.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* m, int x, int y, int z,
+                                         uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+      : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 r;
@@ -115,6 +119,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                : "r"(a)
                : "memory");
+  return r;
+}
+__device__ __forceinline__ float lds32(uint32_t a) {
+  float r;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(a) : "memory");
   return r;
 }
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
@@ -125,13 +134,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-// Two bf16 values, infinities (and NaN) replaced by the largest finite value
-// of their sign.
-__device__ __forceinline__ uint32_t finite(uint32_t x) {
-  uint32_t r;
-  asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7F7F7F7Fu));
   return r;
 }
 // Two E4M3 codes (low 16 bits) -> two f16, exact.
@@ -148,86 +150,118 @@ __device__ __forceinline__ uint32_t f2_to_h2(float a, float b) {
 __device__ __forceinline__ float2 h2_to_f2(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
+// Untiled bulk copy to a shared-memory address (bytes a multiple of 16, both
+// addresses 16-byte aligned).
+__device__ __forceinline__ void bulk_u32(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
+                                         uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
 // 2^e for a normal exponent.
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
-// A warp's place in the list of tiles: sequence, KV head, tile of it.
-struct Place {
-  int b, g, tile, tiles;  // tiles: of one (sequence, KV head)
-  int lo, len;            // rows [lo, len)
-  __device__ __forceinline__ int row0() const { return (lo & ~(kTile - 1)) + tile * kTile; }
+// Shape of the kernel for one head dimension and cache type.
+template <int D, bool FP8>
+struct Cfg {
+  static constexpr int ES = FP8 ? 1 : 2;                   // bytes of an element
+  // 16-row blocks of a tile (and of one softmax update), tiles of 8 KB: more
+  // than one block spreads the update's fixed work and gives independent
+  // chains, but 16 KB tiles would leave the ring too few slots
+  static constexpr int NS = D * ES == 256 ? 1 : 2;
+  static constexpr int TR = 16 * NS;                       // rows of a tile
+  static constexpr int HB = TR * D * ES;                   // bytes of its K (or V) rows
+  static constexpr int SB = FP8 ? 2 * TR * 4 : 0;          // bytes of its scales
+  static constexpr int CTAS = KCF(D, FP8);                 // CTAs of an SM
+  static constexpr int ROOM = (227 * 1024 / CTAS - 3072) / kWarps;   // a warp's share
+  static constexpr int S = ROOM / (2 * HB + SB) < 8 ? ROOM / (2 * HB + SB) : 8;  // ring slots
+  static constexpr int SMEM = 1024 + kWarps * S * (2 * HB + SB);
 };
 
+// A warp's place in the list of tiles: sequence, tile of it.
+struct Place {
+  int b, tile, tiles;     // tiles: of this sequence
+  int lo, len;            // rows [lo, len)
+};
+template <int TR>
+__device__ __forceinline__ int row0(const Place& p) {
+  return (p.lo & ~(TR - 1)) + p.tile * TR;
+}
+template <int TR>
 __device__ __forceinline__ int tiles_of(const PagedArgs& a, int n, int& lo) {
   lo = a.window > 0 && n > a.window ? n - a.window : 0;
   if (n < 1 || n > a.max_rows) return 0;
-  return (n - (lo & ~(kTile - 1)) + kTile - 1) / kTile;
+  return (n - (lo & ~(TR - 1)) + TR - 1) / TR;
 }
+template <int TR>
 __device__ __forceinline__ void enter(const PagedArgs& a, Place& p) {
-  p.g = 0;
   p.tile = 0;
   p.tiles = 0;
   while (p.b < a.B) {
     p.len = a.rows[p.b];
-    p.tiles = tiles_of(a, p.len, p.lo);
+    p.tiles = tiles_of<TR>(a, p.len, p.lo);
     if (p.tiles) return;
     ++p.b;
   }
 }
+template <int TR>
 __device__ __forceinline__ void next(const PagedArgs& a, Place& p) {
   if (++p.tile < p.tiles) return;
-  p.tile = 0;
-  if (++p.g < a.Hkv) return;
   ++p.b;
-  enter(a, p);
+  enter<TR>(a, p);
 }
 
-// Bytes of one tile in a warp's ring (K and V pieces, then E4M3 row scales).
-template <int D, bool FP8>
-constexpr int tile_bytes() {
-  return FP8 ? 2 * kTile * D + kTile * 8 : 2 * kTile * D * 2;
-}
-template <int D, bool FP8>
-constexpr int stages() {
-  return FP8 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : 6);
-}
+// Row of an octet that M index i stands for.
+__device__ __forceinline__ int row_of(int i) { return i ^ ((i & 1) << 2); }
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kThreads, 2) paged_kernel(const PagedArgs a) {
-  constexpr int S = stages<D, FP8>();
-  constexpr int TB = tile_bytes<D, FP8>();
-  constexpr int ES = FP8 ? 1 : 2;               // bytes of an element
+__global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) paged_kernel(
+    const PagedArgs a, const __grid_constant__ CUtensorMap kmap,
+    const __grid_constant__ CUtensorMap vmap) {
+  using C = Cfg<D, FP8>;
+  constexpr int S = C::S, NS = C::NS, TR = C::TR, ES = C::ES, HB = C::HB, TB = 2 * HB;
+  constexpr int RB = D * ES < 128 ? D * ES : 128;  // bytes of a row in a box
+  constexpr int NB = D * ES / RB;               // boxes across a row
   constexpr int KP = D * ES / 64;               // 16-byte pieces of a K row per lane
   constexpr int MT = D / 16;                    // M tiles of V^T
   constexpr int VB = D * ES / 8 >= 16 ? 16 : 8; // bytes of a V piece
   constexpr int VP = D * ES / 8 / VB;           // pieces of a V row per lane
-  constexpr int KBYTES = kTile * D * ES;
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int NO = TR / 8;                    // row octets of a tile
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t s_bar[kWarps][S];
   __shared__ long long s_sum[kWarps];
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g8 = lane >> 2, t4 = lane & 3;
-  const int nwarps = gridDim.x * kWarps;
   const int me = blockIdx.x * kWarps + warp;
+  // neighbouring warps take the KV heads of the same rows
+  const int workers = gridDim.x * kWarps / a.Hkv;
+  const int worker = me / a.Hkv, g = me % a.Hkv;
+  const uint32_t smem = (smem_u32(smem_raw) + 1023) & ~1023u;
+  if (lane == 0) {
+    for (int i = 0; i < S; ++i) mbar_init(&s_bar[warp][i], 1);
+    fence_mbar_init();
+  }
   pdl_trigger();
 
-  // The runs: total tiles, then this warp's first sequence.
+  // The runs: all tiles, then this warp's first one.
   long long total = 0;
   {
     long long sum = 0;
     int lo;
-    for (int b = threadIdx.x; b < a.B; b += kThreads) sum += tiles_of(a, a.rows[b], lo);
+    for (int b = threadIdx.x; b < a.B; b += kThreads) sum += tiles_of<TR>(a, a.rows[b], lo);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) s_sum[warp] = sum;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) total += s_sum[w];
-    total *= a.Hkv;
   }
-  const long long run = (total + nwarps - 1) / nwarps;
-  const long long first = me * run;
-  if (first >= total) return;
+  const long long run = (total + workers - 1) / workers;
+  const long long first = worker * run;
+  if (worker >= workers || first >= total) return;
   const int count = static_cast<int>(min(run, total - first));
   // (each warp scans for itself: 32 sequences at a time)
   long long base = 0;
@@ -236,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kernel(const PagedArgs a) {
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     int lo;
     const int b = b0 + lane;
-    const long long n = b < a.B ? static_cast<long long>(tiles_of(a, a.rows[b], lo)) * a.Hkv : 0;
+    const long long n = b < a.B ? tiles_of<TR>(a, a.rows[b], lo) : 0;
     long long inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -252,83 +286,73 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kernel(const PagedArgs a) {
     }
     base += __shfl_sync(0xffffffffu, inc, 31);
   }
-  enter(a, ip);
-  ip.g = static_cast<int>((first - base) / ip.tiles);
-  ip.tile = static_cast<int>((first - base) % ip.tiles);
+  enter<TR>(a, ip);
+  ip.tile = static_cast<int>(first - base);
   Place cp = ip;
 
   // ---- issue side: tile i of the run into ring slot i % S
-  const uint32_t ring = smem_u32(smem) + warp * (S * TB);
-  const int page_mask = (1 << a.pool.shift) - 1;
-  int ids[2];       // page ids of the next tile's two row octets (-1: nothing needed)
+  const uint32_t ring = smem + warp * (S * TB);
+  const uint32_t scales = smem + kWarps * (S * TB) + warp * (S * C::SB);
+  const int P = 1 << a.pool.shift;
+  const int BR = min(P, TR);   // rows of a box: a tile is 1 to 4 boxes, each in one page
+  const uint64_t policy = policy_evict_first();
+  int ids[NO];      // page ids of the next tile's boxes (-2: not needed)
   unsigned bad = 0; // bit s: the tile in slot s named a page out of range
   auto fetch_ids = [&]() {
-    const int r0 = ip.row0();
+    const int r0 = row0<TR>(ip);
     const int32_t* row = a.table + static_cast<long long>(ip.b) * a.width;
 #pragma unroll
-    for (int o = 0; o < 2; ++o) {
-      const int r = r0 + 8 * o;
-      ids[o] = (r + 7 >= ip.lo && r < ip.len) ? row[r >> a.pool.shift] : -2;
+    for (int o = 0; o < NO; ++o) {
+      const int r = r0 + BR * o;
+      ids[o] = (o * BR < TR && r + BR > ip.lo && r < ip.len) ? row[r >> a.pool.shift] : -2;
     }
   };
   int issued = 0;
   auto issue = [&]() {
-    if (issued < count) {
-      const int slot = issued % S;
-      const uint32_t dst = ring + slot * TB;
-      const int r0 = ip.row0();
-      bool use[2];
-      const uint8_t *kp[2], *vp[2];
-      long long srow[2];
-      unsigned wrong = 0;
+    if (issued >= count) return;
+    const int slot = issued % S;
+    unsigned wrong = 0;
+    int boxes = 0;
 #pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const bool ok = ids[o] >= 0 && ids[o] < a.pool.n_pages;
-        if (!ok && ids[o] != -2) wrong = 1;
-        use[o] = ok;
-        const long long e =
-            ok ? ids[o] * a.pool.page_stride +
-                     ((static_cast<long long>(ip.g) << a.pool.shift) + ((r0 + 8 * o) & page_mask)) * D
-               : 0;
-        kp[o] = a.pool.k + e * ES;
-        vp[o] = a.pool.v + e * ES;
-        srow[o] = e / D;
+    for (int o = 0; o < NO; ++o)
+      if (ids[o] != -2) {
+        ++boxes;
+        if (ids[o] < 0 || ids[o] >= a.pool.n_pages) wrong = 1;
       }
-      bad = (bad & ~(1u << slot)) | (wrong << slot);
-      auto in = [&](int r) { return r >= ip.lo && r < ip.len; };
+    bad = (bad & ~(1u << slot)) | (wrong << slot);
+    if (lane == 0) {
+      const uint32_t bar = smem_u32(&s_bar[warp][slot]);
+      const uint32_t dst = ring + slot * TB, sdst = scales + slot * C::SB;
+      constexpr int row_total = 2 * D * ES + (FP8 ? 8 : 0);   // bytes of a K and V row
+      if (wrong) {
+        mbar_arrive(&s_bar[warp][slot]);
+      } else {
+        mbar_arrive_expect_tx(&s_bar[warp][slot], boxes * BR * row_total);
+        const int y = (g << a.pool.shift) + (row0<TR>(ip) & (P - 1));
 #pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const bool ok = use[o] && in(r0 + 8 * o + g8);
+        for (int o = 0; o < NO; ++o) {
+          if (ids[o] == -2) continue;
+          // (boxes of one tile lie in different pages: at the same rows of them)
+          const uint32_t at = dst + o * BR * RB;
 #pragma unroll
-        for (int c = 0; c < KP; ++c)
-          copy_async<16>(dst + ((o * KP + c) * 32 + lane) * 16,
-                         kp[o] + (ok ? g8 * (D * ES) + (4 * c + t4) * 16 : 0), ok);
-      }
-#pragma unroll
-      for (int o = 0; o < 2; ++o)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 2 * t4 + e;
-          const bool ok = use[o] && in(r0 + 8 * o + r);
-#pragma unroll
-          for (int c = 0; c < VP; ++c)
-            copy_async<VB>(dst + KBYTES + (((o * 2 + e) * VP + c) * 32 + lane) * VB,
-                           vp[o] + (ok ? r * (D * ES) + (8 * c + g8) * VB : 0), ok);
+          for (int h = 0; h < NB; ++h) {
+            load_box(at + h * (TR * RB), &kmap, h * 64, y, ids[o], bar, policy);
+            load_box(at + HB + h * (TR * RB), &vmap, h * 64, y, ids[o], bar, policy);
+          }
+          if constexpr (FP8) {
+            const long long e = ids[o] * (a.pool.page_stride / D) + y;
+            bulk_u32(sdst + o * BR * 4, a.pool.ks + e, BR * 4, bar, policy);
+            bulk_u32(sdst + (TR + o * BR) * 4, a.pool.vs + e, BR * 4, bar, policy);
+          }
         }
-      if constexpr (FP8) {
-        // row g8's four scales (K and V of rows g8 and g8 + 8), one a lane
-        const int o = t4 & 1;
-        const bool ok = use[o] && in(r0 + 8 * o + g8);
-        copy_async<4>(dst + 2 * KBYTES + lane * 4,
-                      (t4 < 2 ? a.pool.ks : a.pool.vs) + (ok ? srow[o] + g8 : 0), ok);
-      }
-      if (++issued < count) {
-        next(a, ip);
-        fetch_ids();
       }
     }
-    copy_commit();
+    if (++issued < count) {
+      next<TR>(a, ip);
+      fetch_ids();
+    }
   };
+  __syncwarp();
   fetch_ids();
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue();
@@ -344,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kernel(const PagedArgs a) {
   int begin = cp.tile;              // first tile of the segment in this run
 
   auto start = [&]() {
-    const uint16_t* qh = a.q + cp.b * a.q_stride + (static_cast<long long>(cp.g) * a.rep + g8) * D;
+    const uint16_t* qh = a.q + cp.b * a.q_stride + (static_cast<long long>(g) * a.rep + g8) * D;
     float up = 1.f;
     if constexpr (FP8) {
       float am = 0.f;
@@ -418,73 +442,122 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kernel(const PagedArgs a) {
     }
   };
 
-  auto tile_step = [&](uint32_t src) {
-    // scores: rows g8 and g8 + 8, heads 2 t4 and 2 t4 + 1
-    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  // where a lane reads in a tile
+  const int ra = row_of(g8), v0 = row_of(2 * t4), v1 = row_of(2 * t4 + 1);
+  auto spot = [](int r, int piece) {   // byte of a 16-byte piece of row r
+    return r * RB + ((RB == 128 ? piece ^ (r & 7) : piece ^ ((r >> 1) & 3)) << 4);
+  };
+  const int koff = spot(ra, t4);
+  const int voff0 = VB == 16 ? spot(v0, g8) : spot(v0, g8 / 2) + (g8 & 1) * 8;
+  const int voff1 = VB == 16 ? spot(v1, g8) : spot(v1, g8 / 2) + (g8 & 1) * 8;
+
+  auto tile_step = [&](uint32_t src, uint32_t ssrc) {
+    const int r0 = row0<TR>(cp);
+    // a tile at an end of the sequence holds rows that are not part of it
+    // (anything may stand there): their p is 0 and their V is made 0
+    const bool edge = r0 < cp.lo || r0 + TR > cp.len;
+    auto in = [&](int r) { return r0 + r >= cp.lo && r0 + r < cp.len; };
+    // scores of block n: rows 16 n + ra (x 0, 1) and 8 further (x 2, 3), heads
+    // 2 t4 (x 0, 2) and 2 t4 + 1 (x 1, 3)
+    float x[NS][4], vs[NS][2];
+    float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-    for (int c = 0; c < KP; ++c) {
-      const uint4 x = lds128(src + (c * 32 + lane) * 16);
-      const uint4 y = lds128(src + ((KP + c) * 32 + lane) * 16);
-      const uint32_t xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w};
-      if constexpr (FP8) {
+    for (int n = 0; n < NS; ++n) {
+      float s[2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mma_f16(s[j & 1], e4m3x2_to_h2(xa[j]), e4m3x2_to_h2(ya[j]), e4m3x2_to_h2(xa[j] >> 16),
-                  e4m3x2_to_h2(ya[j] >> 16), qb[c * 8 + 2 * j], qb[c * 8 + 2 * j + 1]);
-      } else {
+      for (int c = 0; c < KP; ++c) {
+        // piece 4 c + t4 of the row
+        const uint32_t at = src + n * 16 * RB +
+                            (RB == 128 ? (c / 2) * (TR * RB) + (koff ^ ((c & 1) << 6)) : koff);
+        const uint4 u = lds128(at), w = lds128(at + 8 * RB);
+        const uint32_t xa[4] = {u.x, u.y, u.z, u.w}, ya[4] = {w.x, w.y, w.z, w.w};
+        if constexpr (FP8) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          mma_bf16(s[j], xa[2 * j], ya[2 * j], xa[2 * j + 1], ya[2 * j + 1], qb[c * 4 + 2 * j],
-                   qb[c * 4 + 2 * j + 1]);
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t k0 = e4m3x2_to_h2(xa[j]), k1 = e4m3x2_to_h2(ya[j]);
+            const uint32_t k2 = e4m3x2_to_h2(xa[j] >> 16), k3 = e4m3x2_to_h2(ya[j] >> 16);
+            if (c == 0 && j < 2)
+              mma<true, true>(s[j], k0, k1, k2, k3, qb[2 * j], qb[2 * j + 1]);
+            else
+              mma<true>(s[j & 1], k0, k1, k2, k3, qb[c * 8 + 2 * j], qb[c * 8 + 2 * j + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (c == 0)
+              mma<false, true>(s[j], xa[2 * j], ya[2 * j], xa[2 * j + 1], ya[2 * j + 1], qb[2 * j],
+                               qb[2 * j + 1]);
+            else
+              mma<false>(s[j], xa[2 * j], ya[2 * j], xa[2 * j + 1], ya[2 * j + 1],
+                         qb[c * 4 + 2 * j], qb[c * 4 + 2 * j + 1]);
+          }
+        }
       }
+      float ks0 = 1.f, ks1 = 1.f;
+      if constexpr (FP8) {
+        const uint32_t at = ssrc + (16 * n + ra) * 4;
+        ks0 = lds32(at);
+        ks1 = lds32(at + 32);
+        vs[n][0] = lds32(at + TR * 4);
+        vs[n][1] = lds32(at + TR * 4 + 32);
+      }
+      x[n][0] = (s[0][0] + s[1][0]) * (sc0 * ks0);
+      x[n][1] = (s[0][1] + s[1][1]) * (sc1 * ks0);
+      x[n][2] = (s[0][2] + s[1][2]) * (sc0 * ks1);
+      x[n][3] = (s[0][3] + s[1][3]) * (sc1 * ks1);
+      if (edge) {
+        if (!in(16 * n + ra)) {
+          x[n][0] = x[n][1] = -INFINITY;
+          vs[n][0] = 0.f;
+        }
+        if (!in(16 * n + ra + 8)) {
+          x[n][2] = x[n][3] = -INFINITY;
+          vs[n][1] = 0.f;
+        }
+      }
+      t0 = fmaxf(t0, fmaxf(x[n][0], x[n][2]));
+      t1 = fmaxf(t1, fmaxf(x[n][1], x[n][3]));
     }
-    float ks0 = 1.f, ks1 = 1.f, vs0 = 1.f, vs1 = 1.f;
-    if constexpr (FP8) {
-      const uint4 f = lds128(src + 2 * KBYTES + g8 * 16);
-      ks0 = __uint_as_float(f.x);
-      ks1 = __uint_as_float(f.y);
-      vs0 = __uint_as_float(f.z);
-      vs1 = __uint_as_float(f.w);
-    }
-    float x0 = (s[0][0] + s[1][0]) * (sc0 * ks0), x1 = (s[0][1] + s[1][1]) * (sc1 * ks0);
-    float x2 = (s[0][2] + s[1][2]) * (sc0 * ks1), x3 = (s[0][3] + s[1][3]) * (sc1 * ks1);
-    const int r0 = cp.row0();
-    if (r0 < cp.lo || r0 + kTile > cp.len) {
-      const int ra = r0 + g8, rb = ra + 8;
-      if (ra < cp.lo || ra >= cp.len) x0 = x1 = -INFINITY;
-      if (rb < cp.lo || rb >= cp.len) x2 = x3 = -INFINITY;
-    }
-    const float t0 = fmaxf(x0, x2), t1 = fmaxf(x1, x3);
-    const bool grow = t0 > m0 || t1 > m1;
-    const bool up = __any_sync(0xffffffffu, grow);
+    const bool up = __any_sync(0xffffffffu, t0 > m0 || t1 > m1);
+    float e0 = 1.f, e1 = 1.f;   // what the sums so far are multiplied by
     if (up) {
       const float n0 = fmaxf(m0, over_rows(t0)), n1 = fmaxf(m1, over_rows(t1));
       // (no score above -inf yet: nothing to rescale)
-      const float e0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0);
-      const float e1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
+      e0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0);
+      e1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
       m0 = n0;
       m1 = n1;
-      l0 *= e0;
-      l1 *= e1;
       w0 *= e0;
       w1 *= e1;
-      rescale(e0, e1);
     }
     // (a maximum of -inf: every score so far is -inf, and p = 2^-inf = 0)
     const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
-    x0 = ex2(x0 - b0);
-    x1 = ex2(x1 - b1);
-    x2 = ex2(x2 - b0);
-    x3 = ex2(x3 - b1);
-    l0 += x0 + x2;
-    l1 += x1 + x3;
-    uint32_t hi0, hi1, lo0, lo1;
+    float p0 = 0.f, p1 = 0.f;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      x[n][0] = ex2(x[n][0] - b0);
+      x[n][1] = ex2(x[n][1] - b1);
+      x[n][2] = ex2(x[n][2] - b0);
+      x[n][3] = ex2(x[n][3] - b1);
+      p0 += x[n][0] + x[n][2];
+      p1 += x[n][1] + x[n][3];
+    }
+    l0 = fmaf(l0, e0, p0);
+    l1 = fmaf(l1, e1, p1);
+    // P^T as B fragments: planes of rows 0-7 and 8-15 of each block
+    constexpr int NP = FP8 ? 2 : 3;
+    uint32_t pb[NS][NP][2];
     if constexpr (FP8) {
-      x0 *= vs0;
-      x1 *= vs0;
-      x2 *= vs1;
-      x3 *= vs1;
-      const float u0 = fmaxf(x0, x2), u1 = fmaxf(x1, x3);
+      float u0 = 0.f, u1 = 0.f;
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        x[n][0] *= vs[n][0];
+        x[n][1] *= vs[n][0];
+        x[n][2] *= vs[n][1];
+        x[n][3] *= vs[n][1];
+        u0 = fmaxf(u0, fmaxf(x[n][0], x[n][2]));
+        u1 = fmaxf(u1, fmaxf(x[n][1], x[n][3]));
+      }
       // the factor keeps the largest p * scale in [2^13, 2^14): set anew
       // when the maximum moved, or when a value would pass 2^15
       if (__any_sync(0xffffffffu, up || u0 * F0 > 32768.f || u1 * F1 > 32768.f)) {
@@ -503,85 +576,117 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kernel(const PagedArgs a) {
         F0 = f0;
         F1 = f1;
       }
-      x0 *= F0;
-      x1 *= F1;
-      x2 *= F0;
-      x3 *= F1;
-      hi0 = f2_to_h2(x0, x1);
-      hi1 = f2_to_h2(x2, x3);
-      const float2 a0 = h2_to_f2(hi0), a1 = h2_to_f2(hi1);
-      lo0 = f2_to_h2(x0 - a0.x, x1 - a0.y);
-      lo1 = f2_to_h2(x2 - a1.x, x3 - a1.y);
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          const float y0 = x[n][2 * o] * F0, y1 = x[n][2 * o + 1] * F1;
+          const uint32_t hi = f2_to_h2(y0, y1);
+          const float2 h = h2_to_f2(hi);
+          pb[n][0][o] = transpose8(hi);
+          pb[n][1][o] = transpose8(f2_to_h2(y0 - h.x, y1 - h.y));
+        }
     } else {
-      hi0 = f2_to_bf16x2(x0, x1);
-      hi1 = f2_to_bf16x2(x2, x3);
-      lo0 = f2_to_bf16x2(x0 - bf16lo(hi0), x1 - bf16hi(hi0));
-      lo1 = f2_to_bf16x2(x2 - bf16lo(hi1), x3 - bf16hi(hi1));
+      // every plane is cut from what the ones before left, and positive where
+      // p is (the floor is below any sum), so an infinite V element stays one
+      auto rest = [](float v, float floor) {
+        return fmaxf(v - __uint_as_float(__float_as_uint(v) & 0xFFFF0000u), floor);
+      };
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          float y0 = x[n][2 * o], y1 = x[n][2 * o + 1];
+          const float f0 = fminf(y0, 0x1p-126f), f1 = fminf(y1, 0x1p-126f);
+#pragma unroll
+          for (int k = 0; k < NP; ++k) {
+            pb[n][k][o] = transpose8(__byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x7632));
+            y0 = rest(y0, f0);
+            y1 = rest(y1, f1);
+          }
+        }
     }
-    hi0 = transpose8(hi0);
-    hi1 = transpose8(hi1);
-    lo0 = transpose8(lo0);
-    lo1 = transpose8(lo1);
-    // V^T: rows 2 t4, 2 t4 + 1 (octet 0) and the same of octet 1
-    const uint32_t vsrc = src + KBYTES;
-    if constexpr (!FP8) {
+    // V^T: the sums of a tile start from zero
+    const uint32_t vsrc = src + HB;
+    auto join = [&](float (&sum)[4], const float (&s)[4]) {
+      sum[0] = fmaf(sum[0], e0, s[0]);
+      sum[1] = fmaf(sum[1], e1, s[1]);
+      sum[2] = fmaf(sum[2], e0, s[2]);
+      sum[3] = fmaf(sum[3], e1, s[3]);
+    };
 #pragma unroll
-      for (int c = 0; c < VP; ++c) {
-        uint4 v[4];
+    for (int c = 0; c < VP; ++c) {
+      constexpr int W = VB / 4;
+      uint32_t v[NS][4][W];   // rows v0, v1, v0 + 8, v1 + 8 of each block
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = lds128(vsrc + ((e * VP + c) * 32 + lane) * 16);
-        const uint32_t x[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w},
-                                  {v[1].x, v[1].y, v[1].z, v[1].w},
-                                  {v[2].x, v[2].y, v[2].z, v[2].w},
-                                  {v[3].x, v[3].y, v[3].z, v[3].w}};
-        // M tile: rows g8 = element 8 g8 + 2 i of this piece, rows g8 + 8 =
-        // the next element
+      for (int n = 0; n < NS; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t a0 = __byte_perm(x[0][i], x[1][i], 0x5410);
-          const uint32_t a1 = __byte_perm(x[0][i], x[1][i], 0x7632);
-          const uint32_t a2 = __byte_perm(x[2][i], x[3][i], 0x5410);
-          const uint32_t a3 = __byte_perm(x[2][i], x[3][i], 0x7632);
-          mma_bf16(acc[c * 4 + i], a0, a1, a2, a3, hi0, hi1);
-          mma_bf16(acc[c * 4 + i], finite(a0), finite(a1), finite(a2), finite(a3), lo0, lo1);
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t at = vsrc + c * (TR * RB) + (16 * n + (e / 2) * 8) * RB + (e & 1 ? voff1 : voff0);
+          if constexpr (VB == 16) {
+            const uint4 u = lds128(at);
+            v[n][e][0] = u.x;
+            v[n][e][1] = u.y;
+            v[n][e][W - 2] = u.z;
+            v[n][e][W - 1] = u.w;
+          } else {
+            const uint2 u = lds64(at);
+            v[n][e][0] = u.x;
+            v[n][e][1] = u.y;
+          }
+          if (edge && !in(16 * n + (e / 2) * 8 + (e & 1 ? v1 : v0))) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[n][e][i] = 0;
+          }
         }
-      }
-    } else {
-      uint32_t x[4][VB / 4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (VB == 16) {
-          const uint4 v = lds128(vsrc + (e * 32 + lane) * 16);
-          x[e][0] = v.x;
-          x[e][1] = v.y;
-          x[e][2] = v.z;
-          x[e][3] = v.w;
+      for (int i = 0; i < W; ++i) {
+        if constexpr (!FP8) {
+          // M tile: rows g8 = element 8 g8 + 2 i of this piece, rows g8 + 8 =
+          // the next element
+          float s[4];
+#pragma unroll
+          for (int n = 0; n < NS; ++n) {
+            const uint32_t a0 = __byte_perm(v[n][0][i], v[n][1][i], 0x5410);
+            const uint32_t a1 = __byte_perm(v[n][0][i], v[n][1][i], 0x7632);
+            const uint32_t a2 = __byte_perm(v[n][2][i], v[n][3][i], 0x5410);
+            const uint32_t a3 = __byte_perm(v[n][2][i], v[n][3][i], 0x7632);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+              if (n == 0 && k == 0)
+                mma<false, true>(s, a0, a1, a2, a3, pb[n][k][0], pb[n][k][1]);
+              else
+                mma<false>(s, a0, a1, a2, a3, pb[n][k][0], pb[n][k][1]);
+            }
+          }
+          join(acc[c * 4 + i], s);
         } else {
-          const uint2 v = lds64(vsrc + (e * 32 + lane) * 8);
-          x[e][0] = v.x;
-          x[e][1] = v.y;
-        }
-      }
+          // codes of two rows side by side: (r0 d0, r1 d0, r0 d1, r1 d1), ...
 #pragma unroll
-      for (int i = 0; i < VB / 4; ++i) {
-        // codes of two rows side by side: (r0 d0, r1 d0, r0 d1, r1 d1), ...
-        const uint32_t p0 = __byte_perm(x[0][i], x[1][i], 0x5140);
-        const uint32_t p1 = __byte_perm(x[0][i], x[1][i], 0x7362);
-        const uint32_t q0 = __byte_perm(x[2][i], x[3][i], 0x5140);
-        const uint32_t q1 = __byte_perm(x[2][i], x[3][i], 0x7362);
+          for (int j = 0; j < 2; ++j) {
+            float s[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t p = j ? p1 : p0, q = j ? q1 : q0;
-          const uint32_t a0 = e4m3x2_to_h2(p), a1 = e4m3x2_to_h2(p >> 16);
-          const uint32_t a2 = e4m3x2_to_h2(q), a3 = e4m3x2_to_h2(q >> 16);
-          mma_f16(acc[2 * i + j], a0, a1, a2, a3, hi0, hi1);
-          mma_f16(acc[2 * i + j], a0, a1, a2, a3, lo0, lo1);
+            for (int n = 0; n < NS; ++n) {
+              const uint32_t p = __byte_perm(v[n][0][i], v[n][1][i], j ? 0x7362 : 0x5140);
+              const uint32_t q = __byte_perm(v[n][2][i], v[n][3][i], j ? 0x7362 : 0x5140);
+              const uint32_t a0 = e4m3x2_to_h2(p), a1 = e4m3x2_to_h2(p >> 16);
+              const uint32_t a2 = e4m3x2_to_h2(q), a3 = e4m3x2_to_h2(q >> 16);
+#pragma unroll
+              for (int k = 0; k < NP; ++k) {
+                if (n == 0 && k == 0)
+                  mma<true, true>(s, a0, a1, a2, a3, pb[n][k][0], pb[n][k][1]);
+                else
+                  mma<true>(s, a0, a1, a2, a3, pb[n][k][0], pb[n][k][1]);
+              }
+            }
+            join(acc[2 * i + j], s);
+          }
         }
       }
     }
   };
 
-  // The segment of (cp.b, cp.g) ends with the current tile.
+  // The run's part of sequence cp.b ends with the current tile.
   auto finish = [&]() {
 #pragma unroll
     for (int o = 4; o <= 16; o <<= 1) {
@@ -590,11 +695,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kernel(const PagedArgs a) {
     }
     const bool whole = begin == 0 && cp.tile + 1 == cp.tiles;
     const int h0 = 2 * t4, h1 = h0 + 1;
-    if (begin == 0 && lane == 0) {
-      // (the other warps of this (sequence, KV head) follow in order)
+    if (begin == 0 && g == 0 && lane == 0) {
+      // (the workers that share this sequence follow in order)
       const long long rest = cp.tiles - (cp.tile + 1);
-      a.desc[static_cast<long long>(cp.b) * a.Hkv + cp.g] =
-          make_int2(me, whole ? 0 : 1 + static_cast<int>((rest + run - 1) / run));
+      a.desc[cp.b] = make_int2(worker, whole ? 0 : 1 + static_cast<int>((rest + run - 1) / run));
     }
     if (whole && poison) return;
     if (FP8) rescale(1.f / F0, 1.f / F1);
@@ -605,12 +709,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kernel(const PagedArgs a) {
     float *o0, *o1;
     float z0 = 1.f, z1 = 1.f;
     if (whole) {
-      o0 = a.out + (static_cast<long long>(cp.b) * a.Hq + static_cast<long long>(cp.g) * a.rep + h0) * D;
+      o0 = a.out + (static_cast<long long>(cp.b) * a.Hq + static_cast<long long>(g) * a.rep + h0) * D;
       o1 = o0 + D;
       z0 = 1.f / l0;
       z1 = 1.f / l1;
       if (g8 == 0 && a.lse) {
-        float* ls = a.lse + static_cast<long long>(cp.b) * a.Hq + static_cast<long long>(cp.g) * a.rep;
+        float* ls = a.lse + static_cast<long long>(cp.b) * a.Hq + static_cast<long long>(g) * a.rep;
         if (h0 < a.rep) ls[h0] = (m0 + log2f(l0)) * 0.6931471805599453f;
         if (h1 < a.rep) ls[h1] = (m1 + log2f(l1)) * 0.6931471805599453f;
       }
@@ -640,25 +744,29 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kernel(const PagedArgs a) {
   };
 
   start();
+  bool late = false;   // a wait ran out: the results are not written
   for (int i = 0; i < count; ++i) {
-    issue();
-    copy_wait<S - 1>();
-    if (FP8) __syncwarp();   // the scales are read by other lanes than copied them
+    if (!late) issue();
     const int slot = i % S;
-    if ((bad >> slot) & 1) {
+    Spin1 sp;
+    while (!mbar_wait(&s_bar[warp][slot], (i / S) & 1, kWaitHintNs))
+      if (late || sp.expired()) {
+        late = true;
+        break;
+      }
+    if (late || ((bad >> slot) & 1)) {
       poison = true;
-      if (a.status && lane == 0) atomicOr(a.status, DEC_DEV_BAD_PAGE);
+      if (a.status && lane == 0) atomicOr(a.status, late ? DEC_DEV_TIMEOUT : DEC_DEV_BAD_PAGE);
     }
-    tile_step(ring + slot * TB);
-    if (FP8) __syncwarp();
+    if (!poison) tile_step(ring + slot * TB, scales + slot * C::SB);
+    __syncwarp();   // the slot may be refilled
     const bool last = cp.tile + 1 == cp.tiles;
     if (last || i + 1 == count) finish();
     if (i + 1 < count) {
-      next(a, cp);
+      next<TR>(a, cp);
       if (last) start();
     }
   }
-  copy_wait<0>();
 }
 
 // Joins the states of one (sequence, query head); also the outputs of empty
@@ -682,7 +790,7 @@ __global__ void __launch_bounds__(128) join_kernel(const PagedArgs a) {
     if (threadIdx.x == 0 && a.lse) a.lse[static_cast<long long>(b) * a.Hq + h] = -INFINITY;
     return;
   }
-  const int2 d = a.desc[static_cast<long long>(b) * a.Hkv + g];
+  const int2 d = a.desc[b];
   if (d.y == 0) return;   // written by its one warp
   const long long stride = static_cast<long long>(a.rep) * (D + 2);
   constexpr int E = D / 32;
@@ -692,7 +800,8 @@ __global__ void __launch_bounds__(128) join_kernel(const PagedArgs a) {
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   for (int i = grp; i < d.y; i += 4) {
     // the first state is its warp's last, the others their warps' first
-    const float* st = a.part + (static_cast<long long>(d.x + i) * 2 + (i == 0)) * stride;
+    const float* st =
+        a.part + ((static_cast<long long>(d.x + i) * a.Hkv + g) * 2 + (i == 0)) * stride;
     const float m = __ldcg(st + a.rep * D + 2 * hh), l = __ldcg(st + a.rep * D + 2 * hh + 1);
     float v[E];
 #pragma unroll
@@ -729,19 +838,65 @@ __global__ void __launch_bounds__(128) join_kernel(const PagedArgs a) {
 }
 
 template <int D, bool FP8>
-cudaError_t launch_paged(const PagedArgs& a, int grid, cudaStream_t s) {
+cudaError_t launch_paged(const PagedArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int grid,
+                         cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  constexpr int smem = kWarps * stages<D, FP8>() * tile_bytes<D, FP8>();
+  constexpr int smem = Cfg<D, FP8>::SMEM;
   cudaError_t e = allow_smem(paged_kernel<D, FP8>, smem, done);
   if (e != cudaSuccess) return e;
-  paged_kernel<D, FP8><<<grid, kThreads, smem, s>>>(a);
+  paged_kernel<D, FP8><<<grid, kThreads, smem, s>>>(a, km, vm);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_dependent(join_kernel<D>, dim3(static_cast<unsigned>(a.B) * a.Hq), dim3(128), 0, s, a);
 }
 
-// CTAs of the grid: two to an SM.
-int paged_grid(int sms) { return 2 * sms; }
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+  static std::atomic<void*> fn{nullptr};
+  void* f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<EncodeTiledFn>(f);
+}
+
+int tile_rows(const dec_pages* p) {
+  if (p->dtype == DEC_KV_FP8_E4M3) return p->head_dim == 128 ? Cfg<128, true>::TR : Cfg<64, true>::TR;
+  return p->head_dim == 128 ? Cfg<128, false>::TR : Cfg<64, false>::TR;
+}
+
+// Rows of the K (or V) pages of one layer: [page][head and row][element], a
+// box = 128 bytes (64 of an E4M3 row of 64) of the rows of a tile in a page.
+bool encode_pool(EncodeTiledFn enc, CUtensorMap* m, const void* base, const dec_pages* p) {
+  const int tile = tile_rows(p);
+  const bool fp8 = p->dtype == DEC_KV_FP8_E4M3;
+  const cuuint64_t es = fp8 ? 1 : 2, D = p->head_dim;
+  const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(p->n_kv_heads) * p->page_rows,
+                              static_cast<cuuint64_t>(p->n_pages)};
+  const cuuint64_t strides[2] = {D * es, static_cast<cuuint64_t>(p->page_stride) * es};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(D * es < 128 ? D : 128 / es),
+                             static_cast<cuuint32_t>(p->page_rows < tile ? p->page_rows : tile), 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             D * es < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTAs of the grid: one wave.
+int paged_grid(const dec_pages* p, int sms) {
+  if (p->dtype == DEC_KV_FP8_E4M3)
+    return sms * (p->head_dim == 128 ? Cfg<128, true>::CTAS : Cfg<64, true>::CTAS);
+  return sms * (p->head_dim == 128 ? Cfg<128, false>::CTAS : Cfg<64, false>::CTAS);
+}
 
 size_t state_bytes(int grid, int rep, int D) {
   return round256(sizeof(float) * static_cast<size_t>(grid) * kWarps * 2 * rep * (D + 2));
@@ -758,9 +913,9 @@ extern "C" size_t dec_paged_attention_workspace_bytes(const dec_pages* pool, int
       n_q_heads % pool->n_kv_heads || n_q_heads / pool->n_kv_heads > kMaxHeads)
     return 0;
   const int sms = device_sms();
-  return state_bytes(paged_grid(sms > 0 ? sms : 148), n_q_heads / pool->n_kv_heads,
+  return state_bytes(paged_grid(pool, sms > 0 ? sms : 148), n_q_heads / pool->n_kv_heads,
                      pool->head_dim) +
-         round256(sizeof(int2) * static_cast<size_t>(batch) * pool->n_kv_heads);
+         round256(sizeof(int2) * static_cast<size_t>(batch));
 }
 
 extern "C" int dec_paged_attention(const dec_pages* pool, const dec_page_map* map, int layer,
@@ -800,15 +955,21 @@ extern "C" int dec_paged_attention(const dec_pages* pool, const dec_page_map* ma
   a.max_rows = map->width * pool->page_rows;
   a.out = out;
   a.lse = lse;
-  const int grid = paged_grid(sms);
+  const int grid = paged_grid(pool, sms);
   a.part = static_cast<float*>(workspace);
   a.desc = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + state_bytes(grid, a.rep, D));
   a.status = status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
+  const EncodeTiledFn enc = encode_tiled();
+  CUtensorMap km, vm;
+  if (!enc || !encode_pool(enc, &km, a.pool.k, pool) || !encode_pool(enc, &vm, a.pool.v, pool))
+    return cuda_failed(cudaErrorInvalidValue);
   if (pool->dtype == DEC_KV_FP8_E4M3)
-    e = D == 128 ? launch_paged<128, true>(a, grid, s) : launch_paged<64, true>(a, grid, s);
+    e = D == 128 ? launch_paged<128, true>(a, km, vm, grid, s)
+                 : launch_paged<64, true>(a, km, vm, grid, s);
   else
-    e = D == 128 ? launch_paged<128, false>(a, grid, s) : launch_paged<64, false>(a, grid, s);
+    e = D == 128 ? launch_paged<128, false>(a, km, vm, grid, s)
+                 : launch_paged<64, false>(a, km, vm, grid, s);
   return e == cudaSuccess ? DEC_OK : cuda_failed(e);
 }

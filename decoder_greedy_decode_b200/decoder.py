@@ -164,7 +164,7 @@ class Decoder:
             raise ValueError(f"{G} groups of {W} beams need a handle and a cache for {G * W} sequences")
         if n_steps < 1:
             raise ValueError("n_steps must be at least 1")
-        with capi.on_device(dev):
+        with torch.cuda.device(dev):
             tok = token_ids.repeat_interleave(W)
             pos = positions.repeat_interleave(W)
             first = torch.arange(G, dtype=torch.int32, device=dev).repeat_interleave(W) * W

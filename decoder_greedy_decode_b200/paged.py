@@ -8,7 +8,7 @@ dec_paged_attention).
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+from typing import Optional
 
 import torch
 
@@ -84,6 +84,8 @@ class PagedKV:
         if self._ws_bytes == 0:
             raise ValueError("unsupported pool or map (page_rows a power of two in 8..1024, "
                              "head_dim 64 or 128, at most 4096 sequences, 16-byte aligned)")
+        self._refs = (ctypes.byref(self.pool), ctypes.byref(self.map))
+        self._status = self.status.data_ptr()
         self._attend_bytes = {}
 
     @classmethod
@@ -109,29 +111,46 @@ class PagedKV:
 
     # (scratch comes from torch's allocator call by call: calls on several
     # streams and several captured graphs never share it)
-    def _scratch(self, nbytes: int) -> torch.Tensor:
-        return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
 
     def resize(self, new_rows: torch.Tensor, stream=None) -> None:
         """Every sequence s holds new_rows[s] rows (int32; negative: as it is)."""
-        capi.check_tensor(new_rows, "new_rows", torch.int32, (self.n_seqs,), self.device)
-        with capi.on_device(self.device), capi.on_stream(stream, self.device):
-            ws = self._scratch(self._ws_bytes)
-            capi.dec_pages_resize(self.pool, self.map, new_rows, ws, self._ws_bytes, self.status)
+        dev = self.device
+        if capi.elsewhere(dev, stream):
+            with capi.guard(dev, stream):
+                return self.resize(new_rows)
+        capi.check_tensor(new_rows, "new_rows", torch.int32, (self.n_seqs,), dev)
+        ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
+        rc = capi.lib().dec_pages_resize(*self._refs, new_rows.data_ptr(), ws.data_ptr(),
+                                         self._ws_bytes, self._status, capi.current_stream_of(dev))
+        if rc:
+            raise capi.DecError(rc, "dec_pages_resize")
 
     def fork(self, parents: torch.Tensor, stream=None) -> None:
         """Sequence s becomes a copy of sequence parents[s] (int32; negative:
         empty), all at once, by sharing pages."""
-        capi.check_tensor(parents, "parents", torch.int32, (self.n_seqs,), self.device)
-        with capi.on_device(self.device), capi.on_stream(stream, self.device):
-            capi.dec_pages_fork(self.pool, self.map, parents, self.status)
+        dev = self.device
+        if capi.elsewhere(dev, stream):
+            with capi.guard(dev, stream):
+                return self.fork(parents)
+        capi.check_tensor(parents, "parents", torch.int32, (self.n_seqs,), dev)
+        rc = capi.lib().dec_pages_fork(*self._refs, parents.data_ptr(), self._status,
+                                       capi.current_stream_of(dev))
+        if rc:
+            raise capi.DecError(rc, "dec_pages_fork")
 
     def compact(self, stream=None) -> torch.Tensor:
         """Live pages move to the lowest numbers; returns their count (int32 [1])."""
-        with capi.on_device(self.device), capi.on_stream(stream, self.device):
-            live = torch.empty(1, dtype=torch.int32, device=self.device)
-            ws = self._scratch(self._ws_bytes)
-            capi.dec_pages_compact(self.pool, self.map, live, ws, self._ws_bytes, self.status)
+        dev = self.device
+        if capi.elsewhere(dev, stream):
+            with capi.guard(dev, stream):
+                return self.compact()
+        live = torch.empty(1, dtype=torch.int32, device=dev)
+        ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
+        rc = capi.lib().dec_pages_compact(*self._refs, live.data_ptr(), ws.data_ptr(),
+                                          self._ws_bytes, self._status,
+                                          capi.current_stream_of(dev))
+        if rc:
+            raise capi.DecError(rc, "dec_pages_compact")
         return live
 
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -142,41 +161,50 @@ class PagedKV:
         """Store the rows k, v [tokens, n_kv_heads, head_dim] of new tokens at
         `positions` of sequences `seqs` (int32; None: token i is sequence i),
         k normalised by k_norm and rotated by `rope`, and q [tokens,
-        n_q_heads, head_dim] likewise into q_out (bf16; made if None), which
+        n_q_heads, head_dim] likewise into q_out (bf16; zeros if None), which
         is returned.  Tokens at negative positions are skipped."""
-        T = k.shape[0]
-        for name, t in (("k", k), ("v", v)) + ((("q", q),) if q is not None else ()):
-            check_heads(t, name)
-            if t.shape[0] != T or t.shape[2] != self.head_dim or t.dtype != k.dtype:
-                raise ValueError(f"{name} must be [{T}, heads, {self.head_dim}] of {k.dtype}")
-        if k.shape[1] != self.n_kv_heads or v.shape[1] != self.n_kv_heads:
-            raise ValueError(f"k and v must have {self.n_kv_heads} heads")
-        capi.same_device(self.device, k=k, v=v, q=q, phases=rope.phases if rope else None)
-        capi.check_tensor(positions, "positions", torch.int32, (T,), self.device)
-        if seqs is not None:
-            capi.check_tensor(seqs, "seqs", torch.int32, (T,), self.device)
-        for name, t in (("q_norm", q_norm), ("k_norm", k_norm)):
-            if t is not None:
-                capi.check_tensor(t, name, torch.bfloat16, (self.head_dim,), self.device)
-        if q is None and q_out is not None:
+        dev = self.device
+        if capi.elsewhere(dev, stream):
+            with capi.guard(dev, stream):
+                return self.append(layer, k, v, positions, seqs, rope, q, q_out, q_norm, k_norm, eps)
+        D, H = self.head_dim, self.n_kv_heads
+        shape = check_heads(k, "k", dev)
+        T = shape[0]
+        if shape != (T, H, D) or check_heads(v, "v", dev) != shape or v.dtype != k.dtype:
+            raise ValueError(f"k and v must be alike, [tokens, {H}, {D}]")
+        capi.check_tensor(positions, "positions", torch.int32, (T,), dev)
+        io = capi.dec_append(T, capi.dtype_code(k, "k"))
+        if q is not None:
+            shape = check_heads(q, "q", dev)
+            if shape[0] != T or shape[2] != D or q.dtype != k.dtype:
+                raise ValueError(f"q must be [{T}, heads, {D}] of {k.dtype}")
+            if q_out is None:
+                q_out = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
+            else:
+                capi.check_tensor(q_out, "q_out", torch.bfloat16, shape, dev)
+            io.n_q_heads, io.q, io.q_stride = shape[1], q.data_ptr(), q.stride(0)
+            io.q_out = q_out.data_ptr()
+        elif q_out is not None:
             raise ValueError("q_out without q")
-        with capi.on_device(self.device), capi.on_stream(stream, self.device):
-            if q is not None:
-                if q_out is None:
-                    q_out = torch.zeros((T, q.shape[1], self.head_dim), dtype=torch.bfloat16,
-                                        device=self.device)
-                else:
-                    capi.check_tensor(q_out, "q_out", torch.bfloat16, q.shape, self.device)
-            io = capi.dec_append(
-                T, capi.dtype_code(k, "k"), 0 if q is None else q.shape[1],
-                None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                0 if q is None else q.stride(0), k.stride(0), v.stride(0),
-                None if q is None else q_out.data_ptr(), positions.data_ptr(),
-                None if seqs is None else seqs.data_ptr(),
-                None if q_norm is None else q_norm.data_ptr(),
-                None if k_norm is None else k_norm.data_ptr(), eps,
-                ctypes.pointer(rope.c) if rope else None)
-            capi.dec_paged_append(self.pool, self.map, layer, io, self.status)
+        io.k, io.k_stride, io.v, io.v_stride = k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0)
+        io.positions, io.eps = positions.data_ptr(), eps
+        if seqs is not None:
+            capi.check_tensor(seqs, "seqs", torch.int32, (T,), dev)
+            io.seqs = seqs.data_ptr()
+        if q_norm is not None:
+            capi.check_tensor(q_norm, "q_norm", torch.bfloat16, (D,), dev)
+            io.q_norm = q_norm.data_ptr()
+        if k_norm is not None:
+            capi.check_tensor(k_norm, "k_norm", torch.bfloat16, (D,), dev)
+            io.k_norm = k_norm.data_ptr()
+        if rope is not None:
+            if rope.device != dev:
+                raise ValueError(f"rope must be on {dev}, got {rope.device}")
+            io.rope = rope.pointer
+        rc = capi.lib().dec_paged_append(*self._refs, layer, ctypes.byref(io), self._status,
+                                         capi.current_stream_of(dev))
+        if rc:
+            raise capi.DecError(rc, "dec_paged_append")
         return q_out
 
     def attend(self, layer: int, q: torch.Tensor, rows: Optional[torch.Tensor] = None,
@@ -187,26 +215,32 @@ class PagedKV:
         sequences 0 .. batch-1, the last `window` of them if that is not 0.
         Returns out fp32 [batch, n_q_heads, head_dim], with return_lse also
         the log of the softmax sums [batch, n_q_heads]."""
-        check_heads(q, "q")
-        B, Hq, D = q.shape
+        dev = self.device
+        if capi.elsewhere(dev, stream):
+            with capi.guard(dev, stream):
+                return self.attend(layer, q, rows, window, out, return_lse)
+        B, Hq, D = shape = check_heads(q, "q", dev)
         if q.dtype != torch.bfloat16 or D != self.head_dim:
             raise ValueError(f"q must be bfloat16 [batch, heads, {self.head_dim}]")
-        capi.same_device(self.device, q=q)
         if rows is not None:
-            capi.check_tensor(rows, "rows", torch.int32, (B,), self.device)
-        if out is not None:
-            capi.check_tensor(out, "out", torch.float32, (B, Hq, D), self.device)
-        with capi.on_device(self.device), capi.on_stream(stream, self.device):
-            nb = self._attend_bytes.get((B, Hq))
-            if nb is None:
-                nb = capi.dec_paged_attention_workspace_bytes(self.pool, B, Hq)
-                self._attend_bytes[(B, Hq)] = nb
-            if out is None:
-                out = torch.empty((B, Hq, D), dtype=torch.float32, device=self.device)
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=self.device) if return_lse else None
-            ws = self._scratch(nb or 256)
-            capi.dec_paged_attention(self.pool, self.map, layer, B, Hq, q, q.stride(0), rows, window,
-                                     out, lse, ws, nb, self.status)
+            capi.check_tensor(rows, "rows", torch.int32, (B,), dev)
+        if out is None:
+            out = torch.empty(shape, dtype=torch.float32, device=dev)
+        else:
+            capi.check_tensor(out, "out", torch.float32, shape, dev)
+        nb = self._attend_bytes.get((B, Hq))
+        if nb is None:
+            nb = capi.dec_paged_attention_workspace_bytes(self.pool, B, Hq)
+            self._attend_bytes[(B, Hq)] = nb
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev) if return_lse else None
+        ws = torch.empty(nb or 256, dtype=torch.uint8, device=dev)
+        rc = capi.lib().dec_paged_attention(
+            *self._refs, layer, B, Hq, q.data_ptr(), q.stride(0),
+            None if rows is None else rows.data_ptr(), window, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), ws.data_ptr(), nb, self._status,
+            capi.current_stream_of(dev))
+        if rc:
+            raise capi.DecError(rc, "dec_paged_attention")
         return (out, lse) if return_lse else out
 
     def check(self) -> int:

@@ -42,6 +42,8 @@ class Rope:
         bits = [p - (1 << 64) if p >= (1 << 63) else p for p in host]
         self.phases = torch.tensor(bits, dtype=torch.int64).to(device)
         self.c = capi.dec_rope(self.phases.data_ptr(), rot_dim, int(self.interleaved), self.mscale)
+        self.device = self.phases.device
+        self.pointer = ctypes.pointer(self.c)
 
     def apply(self, x: torch.Tensor, positions: torch.Tensor, out: Optional[torch.Tensor] = None,
               stream=None) -> torch.Tensor:
@@ -49,21 +51,29 @@ class Rope:
         any token stride that is a multiple of 4) by int32 positions [tokens]
         into `out` (which may be x).  The row of a token at a negative position
         is copied as it is."""
-        check_heads(x, "x")
-        if out is not None and (out.shape != x.shape or out.dtype != x.dtype):
+        dev = self.device
+        if capi.elsewhere(dev, stream):
+            with capi.guard(dev, stream):
+                return self.apply(x, positions, out)
+        T, H, D = check_heads(x, "x", dev)
+        if out is None:
+            out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
+        elif out.dtype != x.dtype or check_heads(out, "out", dev) != (T, H, D):
             raise ValueError("out must have the shape and type of x")
-        if out is not None:
-            check_heads(out, "out")
-        capi.check_tensor(positions, "positions", torch.int32, (x.shape[0],), x.device)
-        capi.same_device(x.device, out=out, phases=self.phases)
-        with capi.on_device(x.device), capi.on_stream(stream, x.device):
-            if out is None:
-                out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            capi.dec_rope_apply(x.shape[0], x.shape[1], x.shape[2], capi.dtype_code(x, "x"), x,
-                                x.stride(0), out, out.stride(0), positions, self.c)
+        capi.check_tensor(positions, "positions", torch.int32, (T,), dev)
+        rc = capi.lib().dec_rope_apply(T, H, D, capi.dtype_code(x, "x"), x.data_ptr(), x.stride(0),
+                                       out.data_ptr(), out.stride(0), positions.data_ptr(),
+                                       self.pointer, capi.current_stream_of(dev))
+        if rc:
+            raise capi.DecError(rc, "dec_rope_apply")
         return out
 
 
-def check_heads(t: torch.Tensor, name: str) -> None:
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError(f"{name} must be [tokens, heads, head_dim] with contiguous heads")
+def check_heads(t: torch.Tensor, name: str, device):
+    """The shape of a tensor [tokens, heads, head_dim] with contiguous heads."""
+    if t.dim() != 3 or t.device != device:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] on {device}")
+    shape, stride = t.shape, t.stride()
+    if stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
+        raise ValueError(f"{name} must have contiguous heads, got strides {stride}")
+    return shape

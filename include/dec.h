@@ -527,15 +527,15 @@ int dec_rope_apply(int n_tokens, int n_heads, int head_dim, int dtype, const voi
  * way, and K and V may share one buffer). */
 typedef struct dec_pages {
   void *k, *v;                 /* device, 16-byte aligned */
-  float *k_scale, *v_scale;    /* device; NULL for bf16 */
+  float *k_scale, *v_scale;    /* device, 16-byte aligned; NULL for bf16 */
   int n_layers;
   int n_pages;
   int page_rows;               /* a power of two, 8..1024 */
-  int n_kv_heads;
+  int n_kv_heads;              /* 1..256 */
   int head_dim;                /* 64 or 128 */
   int dtype;                   /* dec_kv_dtype */
-  long long layer_stride;      /* elements, multiples of head_dim, at least */
-  long long page_stride;       /* n_kv_heads * page_rows * head_dim */
+  long long layer_stride;      /* elements, multiples of head_dim (E4M3: of */
+  long long page_stride;       /* 4 head_dim), >= kv heads * rows * head_dim */
 } dec_pages;
 
 /* Which pages hold which sequence (device arrays, caller-owned).  Entry j of
@@ -644,7 +644,7 @@ size_t dec_paged_attention_workspace_bytes(const dec_pages *pool, int batch, int
  *              rows all lie before them are not read and may be -1)
  *   out        fp32 [batch, n_q_heads, head_dim]
  *   lse        fp32 [batch, n_q_heads] or NULL
- * Rows outside the range are not read.  n_q_heads / n_kv_heads <= 8.  The
+ * What stands in rows outside the range does not matter.  n_q_heads / n_kv_heads <= 8.  The
  * work is split evenly over the GPU by the lengths on the device, whatever
  * their mix.  rows[b] < 0 or behind the table's end raises
  * DEC_DEV_BAD_POSITION, an unassigned page DEC_DEV_BAD_PAGE; that sequence's

@@ -30,7 +30,8 @@ BAD_POOLS = [
     (dict(page_rows=0), -2), (dict(n_layers=0), -2), (dict(n_pages=0), -2), (dict(n_kv_heads=0), -2),
     (dict(page_stride=8 * 16 * 128 - 128), -2), (dict(layer_stride=0), -2),
     (dict(page_stride=8 * 16 * 128 + 8), -2), (dict(k=P + 8), -6),
-    (dict(dtype=1, k_scale=P, v_scale=P + 2), -6),
+    (dict(dtype=1, k_scale=P, v_scale=P + 8), -6),
+    (dict(dtype=1, k_scale=P, v_scale=P, page_stride=8 * 16 * 128 + 128), -6), (dict(n_kv_heads=257), -2),
 ]
 BAD_MAPS = [(dict(table=None), -1), (dict(rows=None), -1), (dict(refs=None), -1), (dict(n_seqs=0), -3),
             (dict(n_seqs=4097), -3), (dict(width=0), -2), (dict(width=1 << 28), -2), (dict(table=P + 2), -6)]
