@@ -7,15 +7,26 @@
 // 2^-33 turns (a product in fp32 is off by p * f_i * 2^-24 radians, i.e. by
 // 0.06 rad at p = 2^20).  The rotation itself is fp32, rounded once.
 //
-// Split.  A warp takes one token and a few of its heads: the lanes hold the
-// sine and cosine of their pairs in registers for all of them, a head row is
-// 32 lanes x 2 pairs (head_dim 128) or 1 pair (64), so RMSNorm and the E4M3
-// row maximum are warp reductions and nothing passes through shared memory.
-// All head rows of a warp are loaded before the first is used (the loads are
-// what bounds the kernel: every input is read once, every output written
-// once).
+// Split.  A warp takes one token and some of its head rows, four at a time:
+// eight lanes hold a row, 16 (head_dim 128) or 8 (64) of its elements each, so
+// loads and stores are 16 bytes a lane and one three-step butterfly reduces
+// four rows (RMSNorm sums, E4M3 maxima).  Nothing passes through shared
+// memory; the sines and cosines of a token are computed once by the warp,
+// each lane a quarter of what its eight lanes need, and kept in registers
+// for all rows.  The next rows are loaded before the present ones are used.
+// The bound is HBM (every input read once, every output written once); with a
+// row per warp and IEEE divisions the issue slots were it (193 instructions a
+// row, 180 us for 16384 tokens with E4M3 pages; floor 36).
+//
+// E4M3 codes are RNE(x / scale) of the IEEE quotient.  The quotient comes from
+// a correctly rounded reciprocal y of the scale by one residual step
+// (Markstein 1990): q0 = x y, q = q0 + (x - q0 scale) y, which is the IEEE
+// quotient while nothing underflows; rows with a maximum outside
+// [2^-60, 2^100] are first brought near 1 by a power of two.
 #include <cuda_runtime.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "dec.h"
 #include "dec_paged.h"
@@ -25,7 +36,7 @@ namespace dec {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kHeadsPerWarp = 4;
+constexpr int kCtas = 5;   // CTAs of an SM (96 registers a thread)
 
 struct RowsArgs {
   int n_tokens, Hq, Hkv;              // Hkv = 0: rotation alone
@@ -45,257 +56,435 @@ struct RowsArgs {
   int* status;
 };
 
-template <typename T>
-__device__ __forceinline__ float ld1(const T* p);
-template <>
-__device__ __forceinline__ float ld1<uint16_t>(const uint16_t* p) { return bf16_to_f(*p); }
-template <>
-__device__ __forceinline__ float ld1<float>(const float* p) { return *p; }
-__device__ __forceinline__ void ld2(const uint16_t* p, float& a, float& b) {
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-  a = bf16lo(w);
-  b = bf16hi(w);
+// Two fp32 operations in one instruction (each rounded as by itself).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 pa, pb, pd;\n\t"
+      "mov.b64 pa, {%2, %3};\n\t"
+      "mov.b64 pb, {%4, %5};\n\t"
+      "mul.rn.f32x2 pd, pa, pb;\n\t"
+      "mov.b64 {%0, %1}, pd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
-__device__ __forceinline__ void ld2(const float* p, float& a, float& b) {
-  const float2 w = *reinterpret_cast<const float2*>(p);
-  a = w.x;
-  b = w.y;
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 pa, pb, pc, pd;\n\t"
+      "mov.b64 pa, {%2, %3};\n\t"
+      "mov.b64 pb, {%4, %5};\n\t"
+      "mov.b64 pc, {%6, %7};\n\t"
+      "fma.rn.f32x2 pd, pa, pb, pc;\n\t"
+      "mov.b64 {%0, %1}, pd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
 }
-__device__ __forceinline__ void st2(uint16_t* p, float a, float b) {
-  *reinterpret_cast<uint32_t*>(p) = f2_to_bf16x2(a, b);
-}
-__device__ __forceinline__ void st2(float* p, float a, float b) {
-  *reinterpret_cast<float2*>(p) = make_float2(a, b);
-}
+
+__device__ __forceinline__ float ld1(const uint16_t* p) { return bf16_to_f(*p); }
+__device__ __forceinline__ float ld1(const float* p) { return *p; }
 __device__ __forceinline__ void st1(uint16_t* p, float a) { *p = f_to_bf16(a); }
 __device__ __forceinline__ void st1(float* p, float a) { *p = a; }
 
-// Which elements a lane holds.  NP pairs a lane; x[2j], x[2j+1] are pair j.
-// Rows whose pairs are neighbours (interleaved pairs, and rows without a
-// rotation) are 2 NP consecutive elements.  Half-split pairs (i, i + R/2) of
-// the rotated part, and the passed part split the same way, start at `lo` and
-// `hi`; with NP = 2 both are two consecutive elements when R is a multiple of
-// 4 (`vec`), else each element is addressed for itself.
-template <int NP>
-struct Slots {
-  bool pairs;      // neighbouring pairs
-  bool vec;
-  int lo[NP], hi[NP];
+// N (8 or 4) consecutive elements as loaded.
+template <typename T, int N>
+struct Raw;
+template <>
+struct Raw<uint16_t, 8> {
+  uint4 w;
+  __device__ __forceinline__ void load(const uint16_t* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float* x) const {
+    x[0] = bf16lo(w.x), x[1] = bf16hi(w.x), x[2] = bf16lo(w.y), x[3] = bf16hi(w.y);
+    x[4] = bf16lo(w.z), x[5] = bf16hi(w.z), x[6] = bf16lo(w.w), x[7] = bf16hi(w.w);
+  }
+};
+template <>
+struct Raw<uint16_t, 4> {
+  uint2 w;
+  __device__ __forceinline__ void load(const uint16_t* p) { w = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void get(float* x) const {
+    x[0] = bf16lo(w.x), x[1] = bf16hi(w.x), x[2] = bf16lo(w.y), x[3] = bf16hi(w.y);
+  }
+};
+template <int N>
+struct Raw<float, N> {
+  float4 w[N / 4];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) w[i] = reinterpret_cast<const float4*>(p)[i];
+  }
+  __device__ __forceinline__ void get(float* x) const {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) x[4 * i] = w[i].x, x[4 * i + 1] = w[i].y, x[4 * i + 2] = w[i].z, x[4 * i + 3] = w[i].w;
+  }
+};
+template <int N>
+__device__ __forceinline__ void put(uint16_t* p, const float* x) {
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) w[i] = f2_to_bf16x2(x[2 * i], x[2 * i + 1]);
+  if constexpr (N == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+template <int N>
+__device__ __forceinline__ void put(float* p, const float* x) {
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i)
+    reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+}
+template <int N>
+__device__ __forceinline__ void put(uint8_t* p, const float* q) {   // quotients -> E4M3
+  uint32_t w[N / 4];
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i)
+    w[i] = f2_to_e4m3x2(q[4 * i], q[4 * i + 1]) |
+           (static_cast<uint32_t>(f2_to_e4m3x2(q[4 * i + 2], q[4 * i + 3])) << 16);
+  if constexpr (N == 8)
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(p) = w[0];
+}
+__device__ __forceinline__ void put1(uint16_t* p, float x) { st1(p, x); }
+__device__ __forceinline__ void put1(float* p, float x) { st1(p, x); }
+__device__ __forceinline__ void put1(uint8_t* p, float q) {
+  *p = static_cast<uint8_t>(f2_to_e4m3x2(q, 0.f));
+}
+
+// Elements of a lane's vectors: 16 bytes of input, or what the lane holds of
+// half a row.
+template <typename T, int D>
+constexpr int vector_of() {
+  return 16 / sizeof(T) < D / 16 ? 16 / sizeof(T) : D / 16;
+}
+
+// Reductions over the eight lanes of a row.
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Element of a row that pair p starts (a) and ends (b).  Half-split pairs
+// (`half`): pair p < R/2 is elements (p, p + R/2), and the passed part is
+// split the same way.  Otherwise (interleaved pairs, rows that are not
+// rotated) pair p is elements 2p and 2p + 1.
+template <int D>
+__device__ __forceinline__ int first_of(int p, int R) {
+  const int r = R >> 1;
+  return p < r ? p : R + (p - r);
+}
+template <int D>
+__device__ __forceinline__ int second_of(int p, int R) {
+  const int r = R >> 1;
+  return p < r ? p + r : R + (D - R) / 2 + (p - r);
+}
+// A lane's 2N = D/8 elements are runs of V consecutive ones, 8 V apart (the
+// eight lanes of a row read 8 V elements side by side): x[k V + e] is element
+// e of run k.  Half-split rows: run k < N/V holds the first elements of pairs
+// 8 V k + V o + e, run k + N/V their second ones.
+template <int D, int V>
+__device__ __forceinline__ int run_at(bool half, int k, int o, int R) {
+  constexpr int K = D / 16 / V;   // runs of first elements
+  if (!half) return (8 * k + o) * V;
+  return k < K ? first_of<D>((8 * k + o) * V, R) : second_of<D>((8 * (k - K) + o) * V, R);
+}
+// Pair that x[j], x[N + j] (half) or x[2j], x[2j + 1] are.
+template <int D, int V>
+__device__ __forceinline__ int pair_at(bool half, int j, int o) {
+  return half ? (8 * (j / V) + o) * V + j % V : ((8 * (2 * j / V) + o) * V + 2 * j % V) / 2;
+}
+
+// How the pairs of a rotated row lie in a lane's registers.
+enum Mode {
+  kHalf,     // half-split pairs, R/2 a multiple of V: x[j] and x[N + j]
+  kPairs,    // neighbours x[2j], x[2j + 1] (interleaved pairs, or no rotation)
+  kScalar    // half-split pairs, any R: as kHalf, but every element for itself
 };
 
-template <int D>
-__device__ __forceinline__ Slots<D / 64> half_slots(int lane, int R) {
-  constexpr int NP = D / 64;
-  Slots<NP> s;
-  s.pairs = false;
-  s.vec = NP == 2 && (R & 3) == 0;
-#pragma unroll
-  for (int j = 0; j < NP; ++j) {
-    const int p = lane * NP + j;
-    const int r = R >> 1;
-    s.lo[j] = p < r ? p : R + (p - r);
-    s.hi[j] = p < r ? p + r : R + (D - R) / 2 + (p - r);
-  }
-  return s;
-}
-template <int D>
-__device__ __forceinline__ Slots<D / 64> pair_slots(int lane) {
-  constexpr int NP = D / 64;
-  Slots<NP> s;
-  s.pairs = true;
-  s.vec = true;
-#pragma unroll
-  for (int j = 0; j < NP; ++j) {
-    s.lo[j] = 2 * (lane * NP + j);
-    s.hi[j] = s.lo[j] + 1;
-  }
-  return s;
-}
+// T: element of q, k and v; TO: of q_out.  CACHE 0: rotation alone; 1: bf16
+// pages; 2: E4M3 pages.
+template <int D, typename T, typename TO, int CACHE, Mode M>
+__global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs a, int per_token) {
+  constexpr int N = D / 16;     // pairs of a lane
+  constexpr int V = vector_of<T, D>(), K = 2 * N / V;
+  const int lane = threadIdx.x & 31, oct = lane >> 3, o = lane & 7;
+  const int rows = a.Hq + 2 * a.Hkv, quads = (rows + 3) / 4;
+  const int r = a.rot >> 1;
+  // A job is a token's quads part, part + per_token, ...; a warp takes jobs
+  // `hop` apart.
+  const int jobs = a.n_tokens * per_token, hop = gridDim.x * kWarps;
+  const int job0 = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (job0 >= jobs) return;
 
-template <int NP, typename T>
-__device__ __forceinline__ void load_row(const T* p, const Slots<NP>& s, float (&x)[2 * NP]) {
-  if (s.pairs) {
+  // section of a row: 0 q, 1 k, 2 v
+  auto section = [&](int i) { return i < a.Hq ? 0 : i < a.Hq + a.Hkv ? 1 : 2; };
+  // (rows that are not rotated are read as neighbours in every mode)
+  auto source = [&](int t, int i, int sec) {
+    return sec == 0   ? static_cast<const T*>(a.q) + t * a.q_stride + i * D
+           : sec == 1 ? static_cast<const T*>(a.k) + t * a.k_stride + (i - a.Hq) * D
+                      : static_cast<const T*>(a.v) + t * a.v_stride + (i - a.Hq - a.Hkv) * D;
+  };
+  auto split = [&](int sec) { return M != kPairs && a.phases && sec < 2; };
+  Raw<T, V> raw[K];   // the next quad, across the tokens of a warp
+  int fjob = job0, ft = job0 / per_token, fquad = job0 % per_token;   // next quad to load
+  auto fetch = [&]() {
+    if (M == kScalar || fjob >= jobs) return;
+    // (behind the last row: the last one again, never written)
+    const int i = min(4 * fquad + oct, rows - 1), sec = section(i);
+    const T* p = source(ft, i, sec);
 #pragma unroll
-    for (int j = 0; j < NP; ++j) ld2(p + s.lo[j], x[2 * j], x[2 * j + 1]);
-  } else if (NP == 2 && s.vec) {
-    ld2(p + s.lo[0], x[0], x[2]);
-    ld2(p + s.hi[0], x[1], x[3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      x[2 * j] = ld1(p + s.lo[j]);
-      x[2 * j + 1] = ld1(p + s.hi[j]);
+    for (int k = 0; k < K; ++k) raw[k].load(p + run_at<D, V>(split(sec), k, o, a.rot));
+    fquad += per_token;
+    if (fquad >= quads) {
+      fjob += hop;
+      ft = fjob / per_token;
+      fquad = fjob % per_token;
     }
-  }
-}
-template <int NP, typename T>
-__device__ __forceinline__ void store_row(T* p, const Slots<NP>& s, const float (&x)[2 * NP]) {
-  if (s.pairs) {
-#pragma unroll
-    for (int j = 0; j < NP; ++j) st2(p + s.lo[j], x[2 * j], x[2 * j + 1]);
-  } else if (NP == 2 && s.vec) {
-    st2(p + s.lo[0], x[0], x[2]);
-    st2(p + s.hi[0], x[1], x[3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      st1(p + s.lo[j], x[2 * j]);
-      st1(p + s.hi[j], x[2 * j + 1]);
-    }
-  }
-}
-// The E4M3 codes of a row (same slots), and its scale.
-template <int NP>
-__device__ __forceinline__ void store_codes(uint8_t* p, float* scale, int lane,
-                                            const Slots<NP>& s, const float (&x)[2 * NP]) {
-  float am = 0.f;
-#pragma unroll
-  for (int j = 0; j < 2 * NP; ++j) am = fmaxf(am, fabsf(x[j]));
-  am = fmaxf(warp_max(am), 1.17549435e-38f);  // 2^-126
-  const float sc = __fdiv_rn(am, 448.0f);
-  if (lane == 0) *scale = sc;
-  uint16_t c[NP];
-#pragma unroll
-  for (int j = 0; j < NP; ++j)
-    c[j] = f2_to_e4m3x2(__fdiv_rn(x[2 * j], sc), __fdiv_rn(x[2 * j + 1], sc));
-  if (s.pairs) {
-#pragma unroll
-    for (int j = 0; j < NP; ++j) *reinterpret_cast<uint16_t*>(p + s.lo[j]) = c[j];
-  } else if (NP == 2 && s.vec) {
-    const uint32_t w = static_cast<uint32_t>(c[0]) | (static_cast<uint32_t>(c[NP - 1]) << 16);
-    *reinterpret_cast<uint16_t*>(p + s.lo[0]) = static_cast<uint16_t>(__byte_perm(w, 0, 0x4420));
-    *reinterpret_cast<uint16_t*>(p + s.hi[0]) = static_cast<uint16_t>(__byte_perm(w, 0, 0x4431));
-  } else {
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      p[s.lo[j]] = static_cast<uint8_t>(c[j]);
-      p[s.hi[j]] = static_cast<uint8_t>(c[j] >> 8);
-    }
-  }
-}
+  };
+  fetch();
 
-// T: element of q, k, v (and of q_out where TO = T).  CACHE 0: rotation alone;
-// 1: bf16 pages; 2: E4M3 pages.
-template <int D, typename T, typename TO, int CACHE>
-__global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsArgs a, int q_units,
-                                                            int k_units, int units) {
-  constexpr int NP = D / 64;
-  const int lane = threadIdx.x & 31;
-  const long long job = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int t = static_cast<int>(job / units);
-  const int u = static_cast<int>(job % units);
-  if (t >= a.n_tokens) return;
-  const int pos = a.positions[t];
-  if (CACHE && pos < 0) return;   // (rotation alone: the row is copied)
+  // position, sequence and page of the present job and of the next one: the
+  // loads of a token's place are hidden behind the rows of the one before
+  struct Spot {
+    int pos, seq, page, bad;
+  };
+  auto look = [&](int job) {
+    Spot w{-1, 0, -1, 0};
+    if (job < jobs) {
+      const int t = job / per_token;
+      w.pos = a.positions[t];
+      if (CACHE) w.seq = a.seqs ? a.seqs[t] : t;
+    }
+    return w;
+  };
+  auto find = [&](Spot& w) {
+    if (!CACHE || w.pos < 0) return;
+    const int slot = w.pos >> a.pool.shift;
+    if (w.seq < 0 || w.seq >= a.n_seqs)
+      w.bad = DEC_DEV_BAD_PAGE;
+    else if (slot >= a.width)
+      w.bad = DEC_DEV_BAD_POSITION;
+    else
+      w.page = a.table[static_cast<long long>(w.seq) * a.width + slot];
+  };
+  Spot now = look(job0), then = look(job0 + hop);
+  find(now);
 
+  uint64_t phase[N / 4];
+#pragma unroll
+  for (int j = 0; j < N / 4; ++j) {
+    const int p = pair_at<D, V>(M != kPairs, oct * (N / 4) + j, o);
+    phase[j] = a.phases && p < r ? a.phases[p] : 0;
+  }
+  uint32_t g[N];                   // the gains of section `gains`, bf16 pairs
+  int gains = -1;
+
+#pragma unroll 1
+  for (int job = job0; job < jobs; job += hop) {
+  const int t = job / per_token, part = job % per_token;
+  const int pos = now.pos;
+  bool keep = !CACHE || pos >= 0;   // (rotation alone: the row of padding is copied)
   long long row0 = 0;   // element of the token's row of head 0 in the pages
-  if (CACHE) {
-    const int seq = a.seqs ? a.seqs[t] : t;
-    const int slot = pos >> a.pool.shift;
-    int page = -1;
-    int bad = 0;
-    if (seq < 0 || seq >= a.n_seqs) {
-      bad = DEC_DEV_BAD_PAGE;
-    } else if (slot >= a.width) {
-      bad = DEC_DEV_BAD_POSITION;
-    } else {
-      page = a.table[static_cast<long long>(seq) * a.width + slot];
-      if (page < 0 || page >= a.pool.n_pages) bad = DEC_DEV_BAD_PAGE;
-    }
+  if (CACHE && keep) {
+    const int bad = now.bad | (!now.bad && (now.page < 0 || now.page >= a.pool.n_pages) ? DEC_DEV_BAD_PAGE : 0);
     if (bad) {
-      if (a.status && lane == 0 && u == 0) atomicOr(a.status, bad);
-      return;
+      if (a.status && lane == 0 && part == 0) atomicOr(a.status, bad);
+      keep = false;
     }
-    row0 = page * a.pool.page_stride + static_cast<long long>(pos & ((1 << a.pool.shift) - 1)) * D;
+    row0 = now.page * a.pool.page_stride + static_cast<long long>(pos & ((1 << a.pool.shift) - 1)) * D;
   }
+  now = then;
+  find(now);
+  then = look(job + 2 * hop);
+  const bool turned = a.phases && pos >= 0;
 
-  // this warp's heads: of q, of k or of v
-  const int part = u < q_units ? 0 : u < q_units + k_units ? 1 : 2;
-  const int h0 = (part == 0 ? u : part == 1 ? u - q_units : u - q_units - k_units) * kHeadsPerWarp;
-  const int nh = min(kHeadsPerWarp, (part == 0 ? a.Hq : a.Hkv) - h0);
-  const bool turn = a.phases && part < 2 && pos >= 0;
-  const Slots<NP> s = turn && !a.inter ? half_slots<D>(lane, a.rot) : pair_slots<D>(lane);
-  const T* src = static_cast<const T*>(part == 0 ? a.q : part == 1 ? a.k : a.v) +
-                 t * (part == 0 ? a.q_stride : part == 1 ? a.k_stride : a.v_stride) +
-                 static_cast<long long>(h0) * D;
-
-  float x[kHeadsPerWarp][2 * NP];
+  // cosine and sine of the lane's pairs, packed as the rotation uses them:
+  // of two neighbouring pairs (half-split), or twice the same pair
+  constexpr int NC = M == kPairs ? N : N / 2;
+  float2 c2[NC], s2[NC], n2[NC];   // cosine, sine, -sine (neighbours: s2 = (-sine, sine))
+  if (turned) {
+    float c[N / 4], s[N / 4];
 #pragma unroll
-  for (int i = 0; i < kHeadsPerWarp; ++i)
-    if (i < nh) load_row<NP>(src + i * D, s, x[i]);
-
-  float cs[NP], sn[NP];
-  if (turn) {
+    for (int j = 0; j < N / 4; ++j) {
+      // the angle in half turns, [-1, 1): the top 32 bits of the fraction
+      const uint64_t ph = phase[j] * static_cast<uint64_t>(pos);
+      sincospif(static_cast<float>(static_cast<int32_t>(ph >> 32)) * 0x1p-31f, &s[j], &c[j]);
+      c[j] *= a.mscale;
+      s[j] *= a.mscale;
+    }
+    float cs[N], sn[N];
 #pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      const int p = lane * NP + j;
-      cs[j] = 1.f;
-      sn[j] = 0.f;
-      if (p < (a.rot >> 1)) {
-        // the angle in half turns, [-1, 1): the top 32 bits of the fraction
-        const uint64_t ph = a.phases[p] * static_cast<uint64_t>(pos);
-        sincospif(static_cast<float>(static_cast<int32_t>(ph >> 32)) * 0x1p-31f, &sn[j], &cs[j]);
-        cs[j] *= a.mscale;
-        sn[j] *= a.mscale;
+    for (int j = 0; j < N; ++j) {
+      cs[j] = __shfl_sync(0xffffffffu, c[j % (N / 4)], j / (N / 4) * 8 + o);
+      sn[j] = __shfl_sync(0xffffffffu, s[j % (N / 4)], j / (N / 4) * 8 + o);
+    }
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      if (M == kPairs) {
+        c2[j] = make_float2(cs[j], cs[j]);
+        s2[j] = make_float2(-sn[j], sn[j]);
+      } else {
+        c2[j] = make_float2(cs[2 * j], cs[2 * j + 1]);
+        s2[j] = make_float2(sn[2 * j], sn[2 * j + 1]);
+        n2[j] = make_float2(-sn[2 * j], -sn[2 * j + 1]);
       }
     }
   }
-  const uint16_t* gain = part == 0 ? a.q_norm : part == 1 ? a.k_norm : nullptr;
-  float g[2 * NP];
-  if (gain) load_row<NP>(gain, s, g);
+  // element of a row that x[i] is
+  auto element = [&](bool half, int i) {
+    if (M != kScalar || !half) return run_at<D, V>(half, i / V, o, a.rot) + i % V;
+    const int p = pair_at<D, V>(true, i % N, o);
+    return i < N ? first_of<D>(p, a.rot) : second_of<D>(p, a.rot);
+  };
+  auto pair = [](const float* v, int i) { return make_float2(v[2 * i], v[2 * i + 1]); };
+  auto set = [](float* v, int i, float2 y) {
+    v[2 * i] = y.x;
+    v[2 * i + 1] = y.y;
+  };
+  const bool whole = 2 * r == D;   // every pair turns
 
+#pragma unroll 1
+  for (int base = 4 * part; base < rows; base += 4 * per_token) {   // rows base .. base + 3
+    const int row = base + oct;
+    const bool live = keep && row < rows;
+    const int sec = section(min(row, rows - 1));
+    const int least = section(base), most = section(min(base + 3, rows - 1));   // of the four
+    const bool half = split(sec);
+    float x[2 * N];
+    if constexpr (M != kScalar) {
 #pragma unroll
-  for (int i = 0; i < kHeadsPerWarp; ++i) {
-    if (i >= nh) break;
-    if (gain) {
-      float ss = 0.f;
+      for (int k = 0; k < K; ++k) raw[k].get(x + k * V);
+      fetch();
+    } else {
+      const T* p = source(t, min(row, rows - 1), sec);
 #pragma unroll
-      for (int e = 0; e < 2 * NP; ++e) ss = fmaf(x[i][e], x[i][e], ss);
-      const float r = rsqrtf(warp_sum(ss) * (1.0f / D) + a.eps);
-#pragma unroll
-      for (int e = 0; e < 2 * NP; ++e) x[i][e] = x[i][e] * r * g[e];
+      for (int i = 0; i < 2 * N; ++i) x[i] = ld1(p + element(half, i));
     }
-    if (turn) {
+    if (least < 2 && (a.q_norm || a.k_norm)) {
+      float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const float p = x[i][2 * j], q = x[i][2 * j + 1];
-        // a passed pair is not multiplied (cos 1, sin 0 would turn an
-        // infinity in it into NaN)
-        if (lane * NP + j < (a.rot >> 1)) {
-          x[i][2 * j] = p * cs[j] - q * sn[j];
-          x[i][2 * j + 1] = q * cs[j] + p * sn[j];
+      for (int i = 0; i < N; ++i) ss = fma2(pair(x, i), pair(x, i), ss);
+      const float f = rsqrtf(row_sum(ss.x + ss.y) * (1.0f / D) + a.eps);
+      const uint16_t* gain = sec == 0 ? a.q_norm : sec == 1 ? a.k_norm : nullptr;
+      if (gain) {
+        if (gains != sec) {
+          gains = sec;
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            g[i] = pack_bf16x2(gain[element(half, 2 * i)], gain[element(half, 2 * i + 1)]);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          set(x, i, mul2(mul2(pair(x, i), make_float2(f, f)), make_float2(bf16lo(g[i]), bf16hi(g[i]))));
+      }
+    }
+    if (turned && sec < 2) {
+      // a passed pair is not multiplied (cosine 1 and sine 0 would turn an
+      // infinity in it into NaN)
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        if constexpr (M == kPairs) {
+          const float2 u = pair(x, j);
+          const float2 y = fma2(make_float2(u.y, u.x), s2[j], mul2(u, c2[j]));
+          if (whole || pair_at<D, V>(false, j, o) < r) set(x, j, y);
+        } else {
+          const float2 u = pair(x, j), v = pair(x, N / 2 + j);
+          const float2 y = fma2(v, n2[j], mul2(u, c2[j]));
+          const float2 z = fma2(u, s2[j], mul2(v, c2[j]));
+          if (whole || pair_at<D, V>(true, 2 * j, o) < r) {
+            x[2 * j] = y.x;
+            x[N + 2 * j] = z.x;
+          }
+          if (whole || pair_at<D, V>(true, 2 * j + 1, o) < r) {
+            x[2 * j + 1] = y.y;
+            x[N + 2 * j + 1] = z.y;
+          }
         }
       }
     }
-    if (part == 0) {
-      store_row<NP>(static_cast<TO*>(a.q_out) + t * a.q_out_stride +
-                        static_cast<long long>(h0 + i) * D,
-                    s, x[i]);
-    } else if (CACHE) {
-      const long long e = row0 + (static_cast<long long>(h0 + i) << a.pool.shift) * D;
-      uint8_t* base = part == 1 ? a.pool.k : a.pool.v;
-      if (CACHE == 1)
-        store_row<NP>(reinterpret_cast<uint16_t*>(base) + e, s, x[i]);
-      else
-        store_codes<NP>(base + e, (part == 1 ? a.pool.ks : a.pool.vs) + e / D, lane, s, x[i]);
+    auto write = [&](auto* p) {
+      using E = typename std::remove_pointer<decltype(p)>::type;
+      if (M != kScalar || !half) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          put<V>(static_cast<E*>(p + run_at<D, V>(half, k, o, a.rot)), x + k * V);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2 * N; ++i) put1(static_cast<E*>(p + element(half, i)), x[i]);
+      }
+    };
+    if (CACHE == 2 && most > 0) {
+      float am = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2 * N; ++i) am = fmaxf(am, fabsf(x[i]));
+      am = fmaxf(row_max(am), 1.17549435e-38f);  // 2^-126
+      if (live && sec > 0) {
+        float sc, den;   // the scale, and the scale times a power of two
+        if (am >= 0x1p-60f && am <= 0x1p100f) {
+          constexpr float y = 1.0f / 448.0f;
+          const float s0 = am * y;
+          den = sc = fmaf(fmaf(-s0, 448.0f, am), y, s0);
+        } else {
+          // far from 1: the row and its scale times a power of two, exact
+          // where a code is not 0 (an infinite scale: 0, or NaN for infinities)
+          sc = __fdiv_rn(am, 448.0f);
+          const float u = am < 1.f ? 0x1p100f : isinf(sc) ? 0.f : 0x1p-60f;
+          den = isinf(sc) ? 1.f : sc * u;
+#pragma unroll
+          for (int i = 0; i < 2 * N; ++i) x[i] *= u;
+        }
+        const float inv = __frcp_rn(den);
+        const float2 inv2 = make_float2(inv, inv), neg2 = make_float2(-den, -den);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float2 v = pair(x, i), q0 = mul2(v, inv2);
+          const float2 q = fma2(fma2(q0, neg2, v), inv2, q0);
+          set(x, i, make_float2(copysignf(q.x, v.x), copysignf(q.y, v.y)));   // (-0 stays -0)
+        }
+        const long long e =
+            row0 + (static_cast<long long>(row - (sec == 1 ? a.Hq : a.Hq + a.Hkv)) << a.pool.shift) * D;
+        write((sec == 1 ? a.pool.k : a.pool.v) + e);
+        if (o == 0) (sec == 1 ? a.pool.ks : a.pool.vs)[e / D] = sc;
+      }
     }
+    if (live && sec == 0)
+      write(static_cast<TO*>(a.q_out) + t * a.q_out_stride + static_cast<long long>(row) * D);
+    if (CACHE == 1 && live && sec > 0) {
+      const long long e =
+          row0 + (static_cast<long long>(row - (sec == 1 ? a.Hq : a.Hq + a.Hkv)) << a.pool.shift) * D;
+      write(reinterpret_cast<uint16_t*>(sec == 1 ? a.pool.k : a.pool.v) + e);
+    }
+  }
   }
 }
 
 template <int D, typename T, typename TO, int CACHE>
-cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s) {
-  const int qu = (a.Hq + kHeadsPerWarp - 1) / kHeadsPerWarp;
-  const int ku = (a.Hkv + kHeadsPerWarp - 1) / kHeadsPerWarp;
-  const int units = qu + 2 * ku;
-  const long long blocks = (static_cast<long long>(a.n_tokens) * units + kWarps - 1) / kWarps;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  rows_kernel<D, T, TO, CACHE><<<static_cast<unsigned>(blocks), kWarps * 32, 0, s>>>(a, qu, ku,
-                                                                                     units);
+cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t s) {
+  // Warps of a token: one when the tokens alone give every SM its warps (the
+  // angles are then computed once a token), up to one for four rows when
+  // there are few tokens and latency counts.
+  const int most = (a.Hq + 2 * a.Hkv + 3) / 4;
+  const long long want = (32ll * sms + a.n_tokens - 1) / a.n_tokens;
+  const int per_token = static_cast<int>(want < 1 ? 1 : want > most ? most : want);
+  const long long jobs = static_cast<long long>(a.n_tokens) * per_token;
+  if (jobs > (1ll << 30)) return cudaErrorInvalidValue;
+  const long long blocks = (jobs + kWarps - 1) / kWarps;
+  const unsigned n = static_cast<unsigned>(blocks < kCtas * sms ? blocks : kCtas * sms);
+  if (!a.phases || a.inter)
+    rows_kernel<D, T, TO, CACHE, kPairs><<<n, kWarps * 32, 0, s>>>(a, per_token);
+  else if (a.rot % (2 * vector_of<T, D>()) == 0)
+    rows_kernel<D, T, TO, CACHE, kHalf><<<n, kWarps * 32, 0, s>>>(a, per_token);
+  else
+    rows_kernel<D, T, TO, CACHE, kScalar><<<n, kWarps * 32, 0, s>>>(a, per_token);
   return cudaGetLastError();
 }
-
-// Elements of T that a tensor of heads must be aligned to: 4 (two pairs).
-bool bad_align(const void* p, int dtype) { return !is_aligned(p, dtype == DEC_BF16 ? 8 : 16); }
 
 int check_rope(const dec_rope* r, int head_dim) {
   if (!r->phases) return DEC_ERR_NULL;
@@ -306,7 +495,7 @@ int check_rope(const dec_rope* r, int head_dim) {
 
 int check_stride(long long stride, int n, int heads, int D) {
   if (n <= 1) return DEC_OK;   // never used
-  if (stride % 4) return DEC_ERR_ALIGN;
+  if (stride % 8) return DEC_ERR_ALIGN;
   if (stride < static_cast<long long>(heads) * D) return DEC_ERR_SHAPE;
   return DEC_OK;
 }
@@ -360,10 +549,12 @@ extern "C" int dec_rope_apply(int n_tokens, int n_heads, int head_dim, int dtype
   if (rc != DEC_OK) return rc;
   if (n_tokens == 0) return DEC_OK;
   if (!x || !out || !positions) return DEC_ERR_NULL;
-  if (bad_align(x, dtype) || bad_align(out, dtype)) return DEC_ERR_ALIGN;
+  if (!is_aligned(x, 16) || !is_aligned(out, 16)) return DEC_ERR_ALIGN;
   if ((rc = check_stride(x_stride, n_tokens, n_heads, head_dim)) != DEC_OK) return rc;
   if ((rc = check_stride(out_stride, n_tokens, n_heads, head_dim)) != DEC_OK) return rc;
   if (x == out && n_tokens > 1 && x_stride != out_stride) return DEC_ERR_ARG;
+  const int sms = device_sms();
+  if (sms < 0) return sms;
   RowsArgs a{};
   a.n_tokens = n_tokens;
   a.Hq = n_heads;
@@ -379,11 +570,11 @@ extern "C" int dec_rope_apply(int n_tokens, int n_heads, int head_dim, int dtype
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dtype == DEC_BF16)
-    e = head_dim == 128 ? launch_rows<128, uint16_t, uint16_t, 0>(a, s)
-                        : launch_rows<64, uint16_t, uint16_t, 0>(a, s);
+    e = head_dim == 128 ? launch_rows<128, uint16_t, uint16_t, 0>(a, sms, s)
+                        : launch_rows<64, uint16_t, uint16_t, 0>(a, sms, s);
   else
-    e = head_dim == 128 ? launch_rows<128, float, float, 0>(a, s)
-                        : launch_rows<64, float, float, 0>(a, s);
+    e = head_dim == 128 ? launch_rows<128, float, float, 0>(a, sms, s)
+                        : launch_rows<64, float, float, 0>(a, sms, s);
   return e == cudaSuccess ? DEC_OK : cuda_failed(e);
 }
 
@@ -403,14 +594,16 @@ extern "C" int dec_paged_append(const dec_pages* pool, const dec_page_map* map, 
   if (!io->k || !io->v || !io->positions) return DEC_ERR_NULL;
   if (io->n_q_heads ? (!io->q || !io->q_out) : (io->q || io->q_out)) return DEC_ERR_NULL;
   if (!(io->eps >= 0.f)) return DEC_ERR_ARG;
-  if (bad_align(io->k, io->dtype) || bad_align(io->v, io->dtype)) return DEC_ERR_ALIGN;
-  if (io->n_q_heads && (bad_align(io->q, io->dtype) || bad_align(io->q_out, DEC_BF16)))
+  if (!is_aligned(io->k, 16) || !is_aligned(io->v, 16)) return DEC_ERR_ALIGN;
+  if (io->n_q_heads && (!is_aligned(io->q, 16) || !is_aligned(io->q_out, 16)))
     return DEC_ERR_ALIGN;
-  if ((io->q_norm && !is_aligned(io->q_norm, 4)) || (io->k_norm && !is_aligned(io->k_norm, 4)))
+  if ((io->q_norm && !is_aligned(io->q_norm, 2)) || (io->k_norm && !is_aligned(io->k_norm, 2)))
     return DEC_ERR_ALIGN;
   if ((rc = check_stride(io->k_stride, n, pool->n_kv_heads, D)) != DEC_OK) return rc;
   if ((rc = check_stride(io->v_stride, n, pool->n_kv_heads, D)) != DEC_OK) return rc;
   if (io->n_q_heads && (rc = check_stride(io->q_stride, n, io->n_q_heads, D)) != DEC_OK) return rc;
+  const int sms = device_sms();
+  if (sms < 0) return sms;
   RowsArgs a{};
   a.n_tokens = n;
   a.Hq = io->n_q_heads;
@@ -444,16 +637,16 @@ extern "C" int dec_paged_append(const dec_pages* pool, const dec_page_map* map, 
   cudaError_t e;
   if (D == 128) {
     if (f32)
-      e = fp8 ? launch_rows<128, float, uint16_t, 2>(a, s) : launch_rows<128, float, uint16_t, 1>(a, s);
+      e = fp8 ? launch_rows<128, float, uint16_t, 2>(a, sms, s) : launch_rows<128, float, uint16_t, 1>(a, sms, s);
     else
-      e = fp8 ? launch_rows<128, uint16_t, uint16_t, 2>(a, s)
-              : launch_rows<128, uint16_t, uint16_t, 1>(a, s);
+      e = fp8 ? launch_rows<128, uint16_t, uint16_t, 2>(a, sms, s)
+              : launch_rows<128, uint16_t, uint16_t, 1>(a, sms, s);
   } else {
     if (f32)
-      e = fp8 ? launch_rows<64, float, uint16_t, 2>(a, s) : launch_rows<64, float, uint16_t, 1>(a, s);
+      e = fp8 ? launch_rows<64, float, uint16_t, 2>(a, sms, s) : launch_rows<64, float, uint16_t, 1>(a, sms, s);
     else
-      e = fp8 ? launch_rows<64, uint16_t, uint16_t, 2>(a, s)
-              : launch_rows<64, uint16_t, uint16_t, 1>(a, s);
+      e = fp8 ? launch_rows<64, uint16_t, uint16_t, 2>(a, sms, s)
+              : launch_rows<64, uint16_t, uint16_t, 1>(a, sms, s);
   }
   return e == cudaSuccess ? DEC_OK : cuda_failed(e);
 }

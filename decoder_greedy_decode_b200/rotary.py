@@ -48,7 +48,7 @@ class Rope:
     def apply(self, x: torch.Tensor, positions: torch.Tensor, out: Optional[torch.Tensor] = None,
               stream=None) -> torch.Tensor:
         """Rotate x [tokens, heads, head_dim] (bf16 or fp32; heads contiguous,
-        any token stride that is a multiple of 4) by int32 positions [tokens]
+        any token stride that is a multiple of 8) by int32 positions [tokens]
         into `out` (which may be x).  The row of a token at a negative position
         is copied as it is."""
         dev = self.device

@@ -501,14 +501,14 @@ typedef struct dec_rope {
 
 /* Rotate the heads of a tensor by their tokens' positions.
  *   x, out     [n_tokens, n_heads, head_dim] of `dtype`, x_stride /
- *              out_stride elements between tokens (multiples of 4, at least
+ *              out_stride elements between tokens (multiples of 8, at least
  *              n_heads * head_dim when n_tokens > 1; heads contiguous);
  *              out may be x (same stride); otherwise they do not overlap
  *   positions  int32 [n_tokens] (device); the row of a token whose position
  *              is negative (padding) is copied as it is
  * The angle is exact to 2^-33 turns at any position, the rotation is fp32,
  * rounded once to `dtype`.  head_dim 64 or 128 (DEC_ERR_SHAPE); x and out
- * 4-element aligned (DEC_ERR_ALIGN).  Asynchronous on `stream`. */
+ * 16-byte aligned (DEC_ERR_ALIGN).  Asynchronous on `stream`. */
 int dec_rope_apply(int n_tokens, int n_heads, int head_dim, int dtype, const void *x,
                    long long x_stride, void *out, long long out_stride,
                    const int32_t *positions, const dec_rope *rope, void *stream);
@@ -595,8 +595,8 @@ int dec_pages_compact(const dec_pages *pool, const dec_page_map *map, int32_t *n
 
 /* One call's rows for dec_paged_append.  q, k and v are [n_tokens, heads,
  * head_dim] of `dtype` with their own element strides between tokens (slices
- * of one projection's output are fine), 4-element aligned, strides multiples
- * of 4. */
+ * of one projection's output are fine), 16-byte aligned, strides multiples
+ * of 8. */
 typedef struct dec_append {
   int n_tokens;
   int dtype;                  /* dec_dtype of q, k and v */

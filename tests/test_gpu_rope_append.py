@@ -196,16 +196,26 @@ def test_append(T, S, width, Hq, kv, D, R, inter, P, norm, dtype, fmt):
         assert torch.equal(got, old.cpu()), name
 
 
-def test_codes_are_the_row_quantisers():
-    """Without norm and rotation the E4M3 rows are dec_kv_quantize_e4m3's, bit
-    for bit (zero rows, tiny and huge values among them)."""
-    T, kv, D = 40, 2, 128
+@pytest.mark.parametrize("D", [64, 128])
+def test_codes_are_the_row_quantisers(D):
+    """Without norm and rotation the E4M3 rows are dec_kv_quantize_e4m3's (IEEE
+    divisions), bit for bit: random rows of every size from the smallest
+    subnormals to infinity, zeros, NaN, and values on rounding ties."""
+    T, kv = 4096, 4
     c = cache(T, 1, kv, D, 8, "fp8")
-    x = torch.randn((T, kv, D))
-    x[0] = 0
-    x[1] *= 1e-40
-    x[2] *= 1e30
-    x[3, 0, 5] = float("nan")
+    g = torch.Generator().manual_seed(D)
+    x = torch.randn((T, kv, D), generator=g) * torch.exp2(torch.rand((T, kv, 1), generator=g) * 280 - 150)
+    mids = torch.arange(0, 0x7E).to(torch.uint8).view(torch.float8_e4m3fn).float()
+    tie = ((mids[1:] + mids[:-1]) / 2)[torch.randint(0, 125, (T // 4, kv, D), generator=g)]
+    sign = torch.where(torch.rand(tie.shape, generator=g) < 0.5, -1.0, 1.0)
+    x[: T // 4] = sign * tie * torch.exp2(torch.randint(-140, 110, (T // 4, kv, 1), generator=g).float())
+    x[: T // 4, :, 0] = 448.0 * x[: T // 4, :, 0].sign() * \
+        (x[: T // 4, :, 1:].abs().amax(-1) / 448.0).clamp(min=1e-44)
+    x[-1] = 0
+    x[-2, 0, 5] = float("nan")
+    x[-3, 1, 9] = float("-inf")
+    x[-4] = 3e38
+    x[-5] = -1e-45
     x = x.cuda()
     c.append(0, x, x, torch.zeros(T, dtype=torch.int32, device="cuda"))
     codes = torch.zeros((T * kv, D), dtype=torch.uint8, device="cuda")
@@ -213,8 +223,8 @@ def test_codes_are_the_row_quantisers():
     capi.dec_kv_quantize_e4m3(x.contiguous(), T * kv, D, codes, scales)
     page = c.table[:, 0].long()
     for pool, sc in ((c.k, c.k_scale), (c.v, c.v_scale)):
+        assert torch.equal(sc[0][page, :, 0].reshape(-1).view(torch.int32), scales.view(torch.int32))
         assert torch.equal(pool[0][page, :, 0].reshape(T * kv, D), codes)
-        assert torch.equal(sc[0][page, :, 0].reshape(-1), scales)
 
 
 def test_bad_tokens_are_skipped_whole():
