@@ -10,7 +10,10 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import capi
+from . import capi, tensors
+
+
+_workspace = {}   # scratch bytes by (groups, beams, vocab, k, device)
 
 
 class Selection(NamedTuple):
@@ -35,8 +38,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = N
     dev = logits.device
     if dev.type != "cuda":
         raise ValueError("logits must be on a CUDA device")
-    if capi.elsewhere(dev, stream):
-        with capi.guard(dev, stream):
+    if tensors.elsewhere(dev, stream):
+        with tensors.guard(dev, stream):
             return beam_select(logits, scores, k, done, eos, out_scores, out_parents, out_tokens,
                                out_done)
     if logits.dim() != 3 or logits.stride(2) != 1:
@@ -47,17 +50,23 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = N
     if G > 1 and W > 1 and logits.stride(0) != W * row:
         raise ValueError("the rows of logits must be equally far apart")
     k = W if k is None else int(k)
-    capi.check_tensor(scores, "scores", torch.float32, (G, W), dev)
+    tensors.check_tensor(scores, "scores", torch.float32, (G, W), dev)
     if done is not None:
-        capi.check_tensor(done, "done", torch.uint8, (G, W), dev)
-    nb = capi.lib().dec_beam_workspace_bytes(G, W, V, k)
-    shape = (G, max(k, 0))
+        tensors.check_tensor(done, "done", torch.uint8, (G, W), dev)
+    nb = _workspace.get((G, W, V, k, dev.index))
+    if nb is None:
+        nb = _workspace[(G, W, V, k, dev.index)] = capi.lib().dec_beam_workspace_bytes(G, W, V, k)
     ws = torch.empty(nb or 256, dtype=torch.uint8, device=dev)
+    shape = (G, max(k, 0))
+    if out_scores is None and out_parents is None and out_tokens is None:
+        # (one allocation for the three)
+        bits, out_parents, out_tokens = torch.empty((3,) + shape, dtype=torch.int32, device=dev).unbind()
+        out_scores = bits.view(torch.float32)
 
     def result(t, name, dtype):
         if t is None:
             return torch.empty(shape, dtype=dtype, device=dev)
-        capi.check_tensor(t, name, dtype, shape, dev)
+        tensors.check_tensor(t, name, dtype, shape, dev)
         return t
 
     out_scores = result(out_scores, "out_scores", torch.float32)
@@ -66,11 +75,11 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = N
     if out_done is not None or eos >= 0:
         out_done = result(out_done, "out_done", torch.uint8)
     rc = capi.lib().dec_beam_select(
-        G, W, V, k, capi.dtype_code(logits, "logits"), logits.data_ptr(), row, scores.data_ptr(),
+        G, W, V, k, tensors.dtype_code(logits, "logits"), logits.data_ptr(), row, scores.data_ptr(),
         None if done is None else done.data_ptr(), eos, out_scores.data_ptr(),
         out_parents.data_ptr(), out_tokens.data_ptr(),
         None if out_done is None else out_done.data_ptr(), ws.data_ptr(), nb,
-        capi.current_stream_of(dev))
+        tensors.current_stream_of(dev))
     if rc:
         raise capi.DecError(rc, "dec_beam_select")
     return Selection(out_scores, out_parents, out_tokens, out_done)
@@ -89,26 +98,26 @@ def kv_reorder(values: torch.Tensor, parents: torch.Tensor, rows: torch.Tensor,
     dev = values.device
     if dev.type != "cuda":
         raise ValueError("values must be on a CUDA device")
-    if capi.elsewhere(dev, stream):
-        with capi.guard(dev, stream):
+    if tensors.elsewhere(dev, stream):
+        with tensors.guard(dev, stream):
             return kv_reorder(values, parents, rows, scales, status)
     if values.dtype == torch.bfloat16 and scales is None:
         code = capi.DEC_KV_BF16
     elif values.dtype == torch.uint8 and scales is not None:
         code = capi.DEC_KV_FP8_E4M3
-        capi.check_tensor(scales, "scales", torch.float32, (L, 2, B, H, ctx), dev)
+        tensors.check_tensor(scales, "scales", torch.float32, (L, 2, B, H, ctx), dev)
     else:
         raise ValueError("values must be bfloat16 without scales, or uint8 codes with scales")
-    capi.check_tensor(values, "values", values.dtype, None, dev)
+    tensors.check_tensor(values, "values", values.dtype, None, dev)
     n = int(parents.numel())
-    capi.check_tensor(parents, "parents", torch.int32, (n,), dev)
-    capi.check_tensor(rows, "rows", torch.int32, (n,), dev)
+    tensors.check_tensor(parents, "parents", torch.int32, (n,), dev)
+    tensors.check_tensor(rows, "rows", torch.int32, (n,), dev)
     if status is not None:
-        capi.check_tensor(status, "status", torch.int32, (1,), dev)
+        tensors.check_tensor(status, "status", torch.int32, (1,), dev)
     rc = capi.lib().dec_kv_reorder(
         L, H, D, code, B, ctx, values.data_ptr(), None if scales is None else scales.data_ptr(), n,
         parents.data_ptr(), rows.data_ptr(), None if status is None else status.data_ptr(),
-        capi.current_stream_of(dev))
+        tensors.current_stream_of(dev))
     if rc:
         raise capi.DecError(rc, "dec_kv_reorder")
 
@@ -119,12 +128,12 @@ def backtrace(parents: torch.Tensor, tokens: torch.Tensor, stream=None) -> torch
     if parents.dim() != 3:
         raise ValueError("parents must be [n_steps, groups, beams]")
     n, G, W = parents.shape
-    capi.check_tensor(parents, "parents", torch.int32, None)
-    capi.check_tensor(tokens, "tokens", torch.int32, (n, G, W), parents.device)
+    tensors.check_tensor(parents, "parents", torch.int32, None)
+    tensors.check_tensor(tokens, "tokens", torch.int32, (n, G, W), parents.device)
     dev = parents.device
-    if capi.elsewhere(dev, stream):
-        with capi.guard(dev, stream):
+    if tensors.elsewhere(dev, stream):
+        with tensors.guard(dev, stream):
             return backtrace(parents, tokens)
     out = torch.empty((G, W, n), dtype=torch.int32, device=dev)
-    capi.dec_beam_backtrace(n, G, W, parents, tokens, out, capi.current_stream_of(dev))
+    capi.dec_beam_backtrace(n, G, W, parents, tokens, out, tensors.current_stream_of(dev))
     return out

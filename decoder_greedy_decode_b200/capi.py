@@ -6,7 +6,6 @@ import of this module's functions raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -192,69 +191,6 @@ def _stream(stream) -> Optional[int]:
         import torch
         return int(torch.cuda.current_stream().cuda_stream)
     return int(getattr(stream, "cuda_stream", stream))
-
-
-# --------------------------------------------- checks of the tensor wrappers
-def check_tensor(t, name: str, dtype, shape=None, device=None) -> None:
-    """`t` is a contiguous CUDA tensor of this type, shape and device."""
-    if t.dtype != dtype or (shape is not None and t.shape != shape) or not t.is_contiguous() \
-            or not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be contiguous {dtype}"
-                         + (f" of shape {tuple(shape)}" if shape is not None else "")
-                         + f" on {device or 'a CUDA device'}, got {t.dtype} {tuple(t.shape)} with "
-                         f"strides {t.stride()} on {t.device}")
-
-
-def same_device(device, **tensors) -> None:
-    if device.type != "cuda":
-        raise ValueError(f"a CUDA device is needed, got {device}")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
-
-
-def dtype_code(t, name: str) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return DEC_BF16
-    if t.dtype == torch.float32:
-        return DEC_F32
-    raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-
-
-class guard:
-    """Makes `device`, and `stream` if it is not None, current: kernels run
-    there and scratch allocated within belongs to that stream."""
-
-    def __init__(self, device, stream):
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        import torch
-        self.stack = contextlib.ExitStack()
-        self.stack.enter_context(torch.cuda.device(self.device))
-        if self.stream is not None:
-            s = self.stream
-            if not isinstance(s, torch.cuda.Stream):
-                s = torch.cuda.ExternalStream(int(getattr(s, "cuda_stream", s)), device=self.device)
-            self.stack.enter_context(torch.cuda.stream(s))
-
-    def __exit__(self, *exc):
-        return self.stack.__exit__(*exc)
-
-
-def elsewhere(device, stream) -> bool:
-    """Whether a call on `device` and `stream` (None: the current one) needs a
-    guard before it can use current_stream_of()."""
-    import torch
-    return stream is not None or torch.cuda.current_device() != device.index
-
-
-def current_stream_of(device) -> int:
-    """The raw current stream of `device`."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # 2 us less than a Stream object
-    return raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream
 
 
 # ------------------------------------------------------------------ C ABI

@@ -4,17 +4,20 @@
 // Selection.  score(w, t) = s_w + x_wt - log sum_t exp(x_wt).  Within a row
 // the order of the scores is the order of the logits, so one pass over the
 // logits finds both what the row's sum needs and the only k candidates it can
-// send: a CTA holds a chunk of a row in registers (all its loads in flight at
-// once: the bound is HBM), reduces (max, sum exp) and picks its k largest.
-// A second, dependent launch joins the chunks of each row, and the rows of
-// each group, in fp64.
+// send: a CTA takes a chunk of a row in batches of 16 logits a thread (the
+// next batch loads while one is used: the bound is HBM), keeps a running
+// (max, sum exp) per thread and picks its k largest.  A second, dependent
+// launch joins the chunks of each row, and the rows of each group, in fp64.
 //
-// The k largest of a chunk.  Keys (order of the logit, then the lower index)
-// are unique 64-bit words.  The k-th largest of the 64 maxima of groups of
-// four threads is a lower bound of the chunk's k-th largest key; only the k
-// groups that reach it look at their elements again, so at most 4 k x
-// (elements per thread) keys are gathered (a few more than k on random
-// logits), and each finds its place by counting the larger ones.
+// The k largest of a chunk.  The k-th largest of the 64 maxima that groups of
+// four threads find in the first batch is a lower bound of the chunk's k-th
+// largest logit; what reaches it is gathered (a few times k on random logits)
+// and finds its place by counting the larger ones, so a logit costs one
+// maximum and one exponential.  Keys (order of the logit, then the lower
+// index) are unique 64-bit words.  Where too much reaches the bound (many
+// equal logits, or -inf for most of a masked vocabulary, or rising ones), the
+// chunk is read again with keys in place of logits: the bound of every batch
+// is then exact enough that at most 64 k keys of a batch are gathered.
 #include <cuda_runtime.h>
 
 #include "dec.h"
@@ -29,7 +32,9 @@ constexpr int kThreads = 256;
 constexpr int kMaxK = 32;
 constexpr int kMaxBeams = 32;
 constexpr int kMaxLists = 128;   // chunks of a row
-constexpr int kBig = 32, kSmall = 8;   // logits per thread
+constexpr int kEach = 16;        // logits of a thread in a batch
+constexpr int kBatch = kThreads * kEach;
+constexpr int kRoom = 4 * kEach * kMaxK;   // gathered keys
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct BeamArgs {
@@ -42,7 +47,7 @@ struct BeamArgs {
   float* out_scores;
   int32_t *out_parents, *out_tokens;
   uint8_t* out_done;
-  int chunks;
+  int chunks, chunk;       // chunks of a row, logits of a chunk
   float2* stat;            // [G W][chunks] (max, sum of exp2((x - max) log2 e))
   unsigned long long* key; // [G W][chunks][k], descending, 0 = none
 };
@@ -57,8 +62,22 @@ __device__ __forceinline__ float logit_of(unsigned long long key) {
 }
 __device__ __forceinline__ float ex2(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// (a + b) c of two values at once (each operation rounded as by itself)
+__device__ __forceinline__ float2 add_mul2(float a0, float a1, float b, float c) {
+  float2 d;
+  asm("{\n\t.reg .b64 pa, pb, pc;\n\t"
+      "mov.b64 pa, {%2, %3};\n\t"
+      "mov.b64 pb, {%4, %4};\n\t"
+      "mov.b64 pc, {%5, %5};\n\t"
+      "add.rn.f32x2 pa, pa, pb;\n\t"
+      "mul.rn.f32x2 pa, pa, pc;\n\t"
+      "mov.b64 {%0, %1}, pa;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+  return d;
 }
 
 template <typename T>
@@ -90,13 +109,13 @@ struct Vec<uint16_t> {
   }
 };
 
-template <typename T, int EPT>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const BeamArgs a) {
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) rows_kernel(const BeamArgs a) {
   constexpr int N = Vec<T>::N;
-  constexpr int CHUNK = kThreads * EPT;
-  extern __shared__ unsigned long long s_key[];   // gathered keys [4 k EPT]
+  __shared__ unsigned long long s_key[kRoom + kMaxK];   // gathered keys, then the best so far
   __shared__ unsigned long long s_max[kThreads / 4];
   __shared__ unsigned long long s_bound;
+  __shared__ float s_low;
   __shared__ float2 s_stat[kThreads / 32];
   __shared__ int s_n;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -106,105 +125,207 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const BeamArgs a) {
   if (r >= static_cast<long long>(a.G) * a.W) return;
   if (a.done && a.done[r]) return;   // its one candidate needs no logits
   const T* row = static_cast<const T*>(a.logits) + r * a.row_stride;
-  // chunks start on 16-byte boundaries: element i of the row is at i + mis
+  // batches start on 16-byte boundaries: element i of the row is at i + mis
   const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
-
-  float x[EPT];
-  float m = -INFINITY;
-  int mi = -1;
-  const int base = c * CHUNK - mis;
+  const int begin = c * a.chunk - mis, end = min(begin + a.chunk, a.V);
+  const int batches = end > begin ? (end - begin + kBatch - 1) / kBatch : 0;
+  // element e of vector j of this thread in batch b
+  auto index = [&](int b, int j) { return begin + b * kBatch + (j * kThreads + tid) * N; };
+  auto load = [&](int b, float (&x)[kEach]) {
+    if (begin + b * kBatch >= 0 && begin + (b + 1) * kBatch <= end) {
 #pragma unroll
-  for (int j = 0; j < EPT / N; ++j) {
-    const int i = base + (j * kThreads + tid) * N;
-    if (i >= 0 && i + N <= a.V) {
-      Vec<T>::load(row + i, &x[j * N]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        x[j * N + e] = i + e >= 0 && i + e < a.V ? Vec<T>::one(row + i + e) : -INFINITY;
+      for (int j = 0; j < kEach / N; ++j) Vec<T>::load(row + index(b, j), &x[j * N]);
+      return;
     }
-  }
+#pragma unroll
+    for (int j = 0; j < kEach / N; ++j) {
+      const int i = index(b, j);
+      if (i >= 0 && i + N <= end) {
+        Vec<T>::load(row + i, &x[j * N]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          x[j * N + e] = i + e >= 0 && i + e < end ? Vec<T>::one(row + i + e) : -INFINITY;
+      }
+    }
+  };
+  auto largest = [&](const float (&x)[kEach]) {
+    float m = x[0];
+#pragma unroll
+    for (int e = 1; e < kEach; ++e) m = fmaxf(m, x[e]);
+    return m;   // (a NaN is skipped)
+  };
+
+  float x[kEach], y[kEach];
+  load(0, x);
+  load(1, y);   // (behind the chunk: -inf)
   if (tid == 0) {
     s_n = 0;
-    s_bound = 0;
+    s_low = -INFINITY;
   }
-  // the thread's largest logit, the first among equals; an element outside
-  // the row is never it unless the thread holds no other
+  {
+    float q = largest(x);
 #pragma unroll
-  for (int j = 0; j < EPT / N; ++j)
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const int i = base + (j * kThreads + tid) * N + e;
-      const bool in = i >= 0 && i < a.V;
-      if (in && (x[j * N + e] > m || (mi < 0 && x[j * N + e] == m))) {
-        m = x[j * N + e];
-        mi = i;
-      }
+    for (int o = 1; o <= 2; o <<= 1) q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, o));
+    float* quads = reinterpret_cast<float*>(s_max);
+    if ((lane & 3) == 0) quads[tid >> 2] = q;
+    __syncthreads();
+    if (tid < kThreads / 4) {
+      const float v = quads[tid];
+      int rank = 0;
+#pragma unroll 16
+      for (int i = 0; i < kThreads / 4; ++i) rank += quads[i] > v || (quads[i] == v && i < tid);
+      if (rank == a.k - 1) s_low = v;
     }
-  // (all -inf, or nothing: the sum is 0; a NaN or +inf makes it NaN)
-  const float ref = m == -INFINITY ? 0.f : m;
-  float s = 0.f;
+    __syncthreads();
+  }
+  const float low = s_low;
+  float m = -INFINITY, s = 0.f;
+  auto use = [&](int b, const float (&v)[kEach]) {
+    const float bm = largest(v);
+    if (bm >= low && low > -INFINITY) {
 #pragma unroll
-  for (int e = 0; e < EPT; ++e) s += ex2((x[e] - ref) * kLog2e);
-  float M = warp_max(m);
-  const float Mr = M == -INFINITY ? 0.f : M;
+      for (int e = 0; e < kEach; ++e)
+        if (v[e] >= low) {
+          const int at = atomicAdd(&s_n, 1);
+          if (at < kRoom) s_key[at] = key_of(v[e], index(b, e / N) + e % N);
+        }
+    }
+    // (all -inf so far: the sum is 0; a NaN or +inf makes it NaN)
+    if (bm > m) {
+      s *= ex2((m - bm) * kLog2e);
+      m = bm;
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int e = 0; e < kEach; e += 2) {
+      const float2 t = add_mul2(v[e], v[e + 1], -ref, kLog2e);
+      s0 += ex2(t.x);
+      s1 += ex2(t.y);
+    }
+    s += s0 + s1;
+  };
+#pragma unroll 1
+  for (int b = 0; b < batches; b += 2) {
+    use(b, x);
+    if (b + 2 < batches) load(b + 2, x);
+    if (b + 1 < batches) {
+      use(b + 1, y);
+      if (b + 3 < batches) load(b + 3, y);
+    }
+  }
+  const float M = warp_max(m);
+  const float ref = m == -INFINITY ? 0.f : m, Mr = M == -INFINITY ? 0.f : M;
   s = warp_sum(m == -INFINITY && s == 0.f ? 0.f : s * ex2((ref - Mr) * kLog2e));
   if (lane == 0) s_stat[warp] = make_float2(M, s);
+  __syncthreads();
 
-  const unsigned long long mine = mi < 0 ? 0ull : key_of(m, mi);
-  unsigned long long quad = mine;
+  int n = s_n;
+  if (!(low > -INFINITY) || n > kRoom) {
+    // Once more, by keys: the best k so far stand behind the gathered ones.
+    unsigned long long* best = s_key + kRoom;
+    if (tid < a.k) best[tid] = 0;
+    for (int b = 0; b < batches; ++b) {
+      load(b, x);
+      // the thread's largest logit, the first among equals
+      float tm = -INFINITY;
+      int ti = -1;
 #pragma unroll
-  for (int o = 1; o <= 2; o <<= 1) {
-    const unsigned long long other = __shfl_xor_sync(0xffffffffu, quad, o);
-    quad = other > quad ? other : quad;
-  }
-  if ((lane & 3) == 0) s_max[tid >> 2] = quad;
-  __syncthreads();
-  if (tid < kThreads / 4) {
-    const unsigned long long q = s_max[tid];
-    int rank = 0;
-#pragma unroll 16
-    for (int i = 0; i < kThreads / 4; ++i) rank += s_max[i] > q;
-    if (q && rank == a.k - 1) s_bound = q;   // (fewer than k groups hold logits: all are gathered)
-  }
-  __syncthreads();
-  const unsigned long long bound = s_bound;
-  if (mine && mine >= bound) {
-    const float low = logit_of(bound);   // (bound 0: NaN, every comparison below fails)
-#pragma unroll
-    for (int j = 0; j < EPT / N; ++j)
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float v = x[j * N + e];
-        const int i = base + (j * kThreads + tid) * N + e;
-        if (!(v < low) && v == v && i >= 0 && i < a.V) {
-          const unsigned long long key = key_of(v, i);
-          if (key >= bound) s_key[atomicAdd(&s_n, 1)] = key;
+      for (int e = 0; e < kEach; ++e) {
+        const int i = index(b, e / N) + e % N;
+        if (i >= 0 && i < end && (x[e] > tm || (ti < 0 && x[e] == tm))) {
+          tm = x[e];
+          ti = i;
         }
       }
-  }
-  __syncthreads();
-  const int n = s_n;
-  unsigned long long* out = a.key + (r * a.chunks + c) * a.k;
-  for (int i = tid; i < n; i += kThreads) {
-    const unsigned long long key = s_key[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += s_key[j] > key;
-    if (rank < a.k) out[rank] = key;
-  }
-  if (tid >= n && tid < a.k) out[tid] = 0;
-  if (tid == 0) {
-    float bm = -INFINITY;
+      const unsigned long long mine = ti < 0 ? 0ull : key_of(tm, ti);
+      unsigned long long quad = mine;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) bm = fmaxf(bm, s_stat[w].x);
-    const float br = bm == -INFINITY ? 0.f : bm;
+      for (int o = 1; o <= 2; o <<= 1) {
+        const unsigned long long other = __shfl_xor_sync(0xffffffffu, quad, o);
+        quad = other > quad ? other : quad;
+      }
+      __syncthreads();   // s_n, s_max and s_key of the batch before have been read
+      if ((lane & 3) == 0) s_max[tid >> 2] = quad;
+      if (tid == 0) {
+        s_n = 0;
+        s_bound = 0;
+      }
+      __syncthreads();
+      if (tid < kThreads / 4) {
+        const unsigned long long q = s_max[tid];
+        int rank = 0;
+#pragma unroll 16
+        for (int i = 0; i < kThreads / 4; ++i) rank += s_max[i] > q;
+        if (q && rank == a.k - 1) s_bound = q;   // (fewer than k groups hold logits: all are gathered)
+      }
+      __syncthreads();
+      const unsigned long long bound = max(s_bound, best[a.k - 1]);
+      if (mine && mine >= bound) {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          const int i = index(b, e / N) + e % N;
+          if (x[e] == x[e] && i >= 0 && i < end) {
+            const unsigned long long key = key_of(x[e], i);
+            if (key >= bound) s_key[atomicAdd(&s_n, 1)] = key;
+          }
+        }
+      }
+      __syncthreads();
+      n = s_n;
+      // the k best of the gathered keys and the best so far
+      const unsigned long long old = tid < a.k ? best[tid] : 0ull;
+      int rank = 0;
+      if (old) {
+        rank = tid;
+        for (int j = 0; j < n; ++j) rank += s_key[j] > old;
+      }
+      __syncthreads();
+      unsigned long long put[kRoom / kThreads + 1];
+      int to[kRoom / kThreads + 1];
+#pragma unroll
+      for (int u = 0; u <= kRoom / kThreads; ++u) {
+        const int i = u < kRoom / kThreads ? tid + u * kThreads : kRoom;
+        to[u] = kMaxK;
+        put[u] = 0;
+        if (u < kRoom / kThreads && i < n) {
+          put[u] = s_key[i];
+          to[u] = 0;
+          for (int j = 0; j < n; ++j) to[u] += s_key[j] > put[u];
+          for (int j = 0; j < a.k; ++j) to[u] += best[j] > put[u];
+        }
+      }
+      __syncthreads();
+      if (old && rank < a.k) best[rank] = old;
+#pragma unroll
+      for (int u = 0; u < kRoom / kThreads; ++u)
+        if (put[u] && to[u] < a.k) best[to[u]] = put[u];
+    }
+    __syncthreads();
+    if (tid < a.k) a.key[(r * a.chunks + c) * a.k + tid] = best[tid];
+  } else {
+    unsigned long long* out = a.key + (r * a.chunks + c) * a.k;
+    for (int i = tid; i < n; i += kThreads) {
+      const unsigned long long key = s_key[i];
+      int rank = 0;
+      for (int j = 0; j < n; ++j) rank += s_key[j] > key;
+      if (rank < a.k) out[rank] = key;
+    }
+    if (tid >= n && tid < a.k) out[tid] = 0;
+  }
+  if (tid == 0) {
+    float cm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) cm = fmaxf(cm, s_stat[w].x);
+    const float cr = cm == -INFINITY ? 0.f : cm;
     float sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       const float2 t = s_stat[w];
-      sum += t.x == -INFINITY ? t.y : t.y * ex2((t.x - br) * kLog2e);
+      sum += t.x == -INFINITY ? t.y : t.y * ex2((t.x - cr) * kLog2e);
     }
-    a.stat[r * a.chunks + c] = make_float2(bm, sum);
+    a.stat[r * a.chunks + c] = make_float2(cm, sum);
   }
 }
 
@@ -220,9 +341,21 @@ __global__ void __launch_bounds__(kThreads) groups_kernel(const BeamArgs a) {
   pdl_wait();
   for (int w = warp; w < a.W; w += kThreads / 32) {
     const long long r = static_cast<long long>(g) * a.W + w;
+    // (loads first: the lists' heads do not wait for the row's sum)
+    const unsigned long long* lists = a.key + r * a.chunks * a.k;
+    unsigned long long head[kMaxLists / 32], then[kMaxLists / 32];
+    int pos[kMaxLists / 32];
     const double own = a.scores[r];
     const bool done = a.done && a.done[r];
     if (lane == 0) s_done[w] = done;
+#pragma unroll
+    for (int i = 0; i < kMaxLists / 32; ++i) {
+      const int c = i * 32 + lane;
+      const bool has = !done && c < a.chunks;
+      head[i] = has ? __ldcg(lists + c * a.k) : 0ull;
+      then[i] = has && a.k > 1 ? __ldcg(lists + c * a.k + 1) : 0ull;
+      pos[i] = 2;
+    }
     bool flat = !(own > ninf);   // -inf or NaN: no candidate above -inf
     double lse = 0.0;
     if (!done && !flat) {
@@ -258,16 +391,6 @@ __global__ void __launch_bounds__(kThreads) groups_kernel(const BeamArgs a) {
         }
       }
       continue;
-    }
-    const unsigned long long* lists = a.key + r * a.chunks * a.k;
-    unsigned long long head[kMaxLists / 32], then[kMaxLists / 32];
-    int pos[kMaxLists / 32];
-#pragma unroll
-    for (int i = 0; i < kMaxLists / 32; ++i) {
-      const int c = i * 32 + lane;
-      head[i] = c < a.chunks ? __ldcg(lists + c * a.k) : 0ull;
-      then[i] = c < a.chunks && a.k > 1 ? __ldcg(lists + c * a.k + 1) : 0ull;
-      pos[i] = 2;
     }
     for (int p = 0; p < a.k; ++p) {
       unsigned long long best = head[0];
@@ -407,17 +530,18 @@ __global__ void backtrace_kernel(int n, int G, int W, const int32_t* parents,
 }
 
 struct Plan {
-  int ept, chunks;
+  int chunks, chunk;
   size_t stat, total;
 };
-// Chunks of 2048 logits while they fill no more than one wave of CTAs (8 to
-// an SM): then latency counts, and more CTAs share a row.  Else 8192.
+// One wave of CTAs (four to an SM), as far as chunks of at least half a
+// batch and at most kMaxLists of them to a row allow.
 Plan plan_of(int rows, int V, int k, int sms) {
   Plan p{};
-  const int per = 8 - 1;   // most elements before the first 16-byte boundary
-  const long long small = (V + per + kThreads * kSmall - 1) / (kThreads * kSmall);
-  p.ept = small <= kMaxLists && small * rows <= 8ll * sms ? kSmall : kBig;
-  p.chunks = (V + per + kThreads * p.ept - 1) / (kThreads * p.ept);
+  const int len = V + 7;   // and the elements before the first 16-byte boundary
+  int want = (4 * sms + rows - 1) / rows;
+  want = want > kMaxLists ? kMaxLists : want;
+  p.chunk = ((len + want - 1) / want + kBatch / 2 - 1) / (kBatch / 2) * (kBatch / 2);
+  p.chunks = (len + p.chunk - 1) / p.chunk;
   p.stat = round256(sizeof(float2) * static_cast<size_t>(rows) * p.chunks);
   p.total = p.stat + round256(sizeof(unsigned long long) * static_cast<size_t>(rows) * p.chunks * k);
   return p;
@@ -428,12 +552,11 @@ bool bad_beams(int groups, int beams, int vocab, int k) {
          vocab < k || vocab > 1000000;
 }
 
-template <typename T, int EPT>
+template <typename T>
 cudaError_t launch_beam_rows(const BeamArgs& a, cudaStream_t s) {
-  const size_t smem = sizeof(unsigned long long) * 4 * a.k * EPT;
   const int rows = a.G * a.W;
   const int y = rows < 32768 ? rows : 32768;
-  rows_kernel<T, EPT><<<dim3(a.chunks, y, (rows + y - 1) / y), kThreads, smem, s>>>(a);
+  rows_kernel<T><<<dim3(a.chunks, y, (rows + y - 1) / y), kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -483,15 +606,12 @@ extern "C" int dec_beam_select(int groups, int beams, int vocab, int k, int dtyp
   a.out_tokens = out_tokens;
   a.out_done = out_done;
   a.chunks = p.chunks;
+  a.chunk = p.chunk;
   a.stat = static_cast<float2*>(workspace);
   a.key = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + p.stat);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (dtype == DEC_BF16)
-    e = p.ept == kSmall ? launch_beam_rows<uint16_t, kSmall>(a, s)
-                        : launch_beam_rows<uint16_t, kBig>(a, s);
-  else
-    e = p.ept == kSmall ? launch_beam_rows<float, kSmall>(a, s) : launch_beam_rows<float, kBig>(a, s);
+  e = dtype == DEC_BF16 ? launch_beam_rows<uint16_t>(a, s) : launch_beam_rows<float>(a, s);
   if (e == cudaSuccess) e = launch_dependent(groups_kernel, dim3(groups), dim3(kThreads), 0, s, a);
   return e == cudaSuccess ? DEC_OK : cuda_failed(e);
 }

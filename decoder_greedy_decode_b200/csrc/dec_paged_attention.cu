@@ -770,71 +770,74 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) paged_kernel(
 }
 
 // Joins the states of one (sequence, query head); also the outputs of empty
-// sequences.  Four groups of 32 lanes take every fourth state.
+// sequences.  The states' weights come first, so that the sums' loads are
+// independent: four groups of 32 lanes take every fourth state.
 template <int D>
 __global__ void __launch_bounds__(128) join_kernel(const PagedArgs a) {
+  extern __shared__ float s_w[];   // [states]
   __shared__ float s_acc[4][D];
-  __shared__ float s_ml[4][2];
+  __shared__ float s_red[4];
   const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
   const int g = h / a.rep, hh = h % a.rep;
-  const int grp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, grp = tid >> 5, lane = tid & 31;
   pdl_wait();
+  const int2 d = a.desc[b];   // (of no use for an empty sequence)
   const int n = a.rows[b];
   float* out = a.out + (static_cast<long long>(b) * a.Hq + h) * D;
+  float* lse = a.lse ? a.lse + static_cast<long long>(b) * a.Hq + h : nullptr;
   if (n < 0 || n > a.max_rows) {
-    if (threadIdx.x == 0 && h == 0 && a.status) atomicOr(a.status, DEC_DEV_BAD_POSITION);
+    if (tid == 0 && h == 0 && a.status) atomicOr(a.status, DEC_DEV_BAD_POSITION);
     return;
   }
   if (n == 0) {
-    if (threadIdx.x < D) out[threadIdx.x] = 0.f;
-    if (threadIdx.x == 0 && a.lse) a.lse[static_cast<long long>(b) * a.Hq + h] = -INFINITY;
+    if (tid < D) out[tid] = 0.f;
+    if (tid == 0 && lse) *lse = -INFINITY;
     return;
   }
-  const int2 d = a.desc[b];
   if (d.y == 0) return;   // written by its one warp
-  const long long stride = static_cast<long long>(a.rep) * (D + 2);
-  constexpr int E = D / 32;
-  float M = -INFINITY, L = 0.f, acc[E];
+  const int rep = a.rep, words = rep * (D + 2);
+  // the first state is its warp's last, the others their warps' first
+  auto state = [&](int i) {
+    return a.part + (static_cast<long long>(d.x + i) * a.Hkv + g) * (2 * words) + (i == 0 ? words : 0);
+  };
+  float m = -INFINITY;
   bool poison = false;
+  for (int i = tid; i < d.y; i += 128) {
+    const float v = __ldcg(state(i) + rep * D + 2 * hh);
+    s_w[i] = v;
+    poison |= v != v;
+    m = fmaxf(m, v);
+  }
+  m = warp_max(m);
+  if (lane == 0) s_red[grp] = m;
+  if (__syncthreads_or(poison)) return;
+  m = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  float l = 0.f;
+  for (int i = tid; i < d.y; i += 128) {
+    const float w = s_w[i] == -INFINITY ? 0.f : ex2(s_w[i] - m);
+    l += __ldcg(state(i) + rep * D + 2 * hh + 1) * w;
+    s_w[i] = w;
+  }
+  l = warp_sum(l);
+  __syncthreads();   // s_red has been read, s_w is complete
+  if (lane == 0) s_red[grp] = l;
+  constexpr int E = D / 32;
+  float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
   for (int i = grp; i < d.y; i += 4) {
-    // the first state is its warp's last, the others their warps' first
-    const float* st =
-        a.part + ((static_cast<long long>(d.x + i) * a.Hkv + g) * 2 + (i == 0)) * stride;
-    const float m = __ldcg(st + a.rep * D + 2 * hh), l = __ldcg(st + a.rep * D + 2 * hh + 1);
-    float v[E];
+    const float* v = state(i) + hh * D + lane;
+    const float w = s_w[i];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = __ldcg(st + hh * D + e * 32 + lane);
-    if (m != m) poison = true;
-    const float nm = fmaxf(M, m);
-    const float e0 = M == -INFINITY ? 0.f : ex2(M - nm), e1 = m == -INFINITY ? 0.f : ex2(m - nm);
-    L = L * e0 + l * e1;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * e0 + v[e] * e1;
-    M = nm;
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(__ldcg(v + 32 * e), w, acc[e]);
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) s_acc[grp][e * 32 + lane] = acc[e];
-  if (lane == 0) {
-    s_ml[grp][0] = M;
-    s_ml[grp][1] = L;
-  }
-  if (__syncthreads_or(poison)) return;
-  if (threadIdx.x < D) {
-    float m = -INFINITY, l = 0.f, x = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmaxf(m, s_ml[i][0]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float e = s_ml[i][0] == -INFINITY ? 0.f : ex2(s_ml[i][0] - m);
-      l += s_ml[i][1] * e;
-      x += s_acc[i][threadIdx.x] * e;
-    }
-    out[threadIdx.x] = x / l;
-    if (threadIdx.x == 0 && a.lse)
-      a.lse[static_cast<long long>(b) * a.Hq + h] = (m + log2f(l)) * 0.6931471805599453f;
-  }
+  __syncthreads();
+  l = s_red[0] + s_red[1] + s_red[2] + s_red[3];
+  if (tid < D) out[tid] = (s_acc[0][tid] + s_acc[1][tid] + s_acc[2][tid] + s_acc[3][tid]) / l;
+  if (tid == 0 && lse) *lse = (m + log2f(l)) * 0.6931471805599453f;
 }
 
 template <int D, bool FP8>
@@ -847,7 +850,9 @@ cudaError_t launch_paged(const PagedArgs& a, const CUtensorMap& km, const CUtens
   paged_kernel<D, FP8><<<grid, kThreads, smem, s>>>(a, km, vm);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_dependent(join_kernel<D>, dim3(static_cast<unsigned>(a.B) * a.Hq), dim3(128), 0, s, a);
+  const size_t states = sizeof(float) * kWarps * grid / a.Hkv;   // at most a worker's each
+  return launch_dependent(join_kernel<D>, dim3(static_cast<unsigned>(a.B) * a.Hq), dim3(128), states,
+                          s, a);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,

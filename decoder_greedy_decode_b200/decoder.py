@@ -9,7 +9,7 @@ from typing import Dict, Optional
 
 import torch
 
-from . import beam, capi
+from . import beam, capi, tensors
 from .synth import LAYER_KEYS, ModelShape
 
 assert tuple(LAYER_KEYS) == tuple(capi.LW_ORDER)
@@ -158,8 +158,8 @@ class Decoder:
         the device as in step (check)."""
         G, W, V = int(token_ids.numel()), beams, self.shape.vocab
         dev = kv.buf.device
-        capi.check_tensor(token_ids, "token_ids", torch.int32, (G,), dev)
-        capi.check_tensor(positions, "positions", torch.int32, (G,), dev)
+        tensors.check_tensor(token_ids, "token_ids", torch.int32, (G,), dev)
+        tensors.check_tensor(positions, "positions", torch.int32, (G,), dev)
         if not 1 <= G * W <= min(self.max_batch, kv.batch):
             raise ValueError(f"{G} groups of {W} beams need a handle and a cache for {G * W} sequences")
         if n_steps < 1:

@@ -12,8 +12,8 @@ from typing import Optional
 
 import torch
 
-from . import capi
-from .rotary import Rope, check_heads
+from . import capi, tensors
+from .rotary import Rope
 
 
 class PagedKV:
@@ -64,13 +64,13 @@ class PagedKV:
                     (self.n_pages > 1 and t.stride(1) * D != ps):
                 raise ValueError(f"{name} must be fp32 with the layout of k's rows")
         self.device = k.device
-        capi.same_device(self.device, v=v, k_scale=k_scale, v_scale=v_scale)
+        tensors.same_device(self.device, v=v, k_scale=k_scale, v_scale=v_scale)
         if table.dim() != 2:
             raise ValueError("table must be [n_seqs, width]")
         self.n_seqs, self.width = table.shape
-        capi.check_tensor(table, "table", torch.int32, None, self.device)
-        capi.check_tensor(rows, "rows", torch.int32, (self.n_seqs,), self.device)
-        capi.check_tensor(refs, "refs", torch.int32, (self.n_pages,), self.device)
+        tensors.check_tensor(table, "table", torch.int32, None, self.device)
+        tensors.check_tensor(rows, "rows", torch.int32, (self.n_seqs,), self.device)
+        tensors.check_tensor(refs, "refs", torch.int32, (self.n_pages,), self.device)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.table, self.rows, self.refs = table, rows, refs
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
@@ -115,13 +115,13 @@ class PagedKV:
     def resize(self, new_rows: torch.Tensor, stream=None) -> None:
         """Every sequence s holds new_rows[s] rows (int32; negative: as it is)."""
         dev = self.device
-        if capi.elsewhere(dev, stream):
-            with capi.guard(dev, stream):
+        if tensors.elsewhere(dev, stream):
+            with tensors.guard(dev, stream):
                 return self.resize(new_rows)
-        capi.check_tensor(new_rows, "new_rows", torch.int32, (self.n_seqs,), dev)
+        tensors.check_tensor(new_rows, "new_rows", torch.int32, (self.n_seqs,), dev)
         ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
         rc = capi.lib().dec_pages_resize(*self._refs, new_rows.data_ptr(), ws.data_ptr(),
-                                         self._ws_bytes, self._status, capi.current_stream_of(dev))
+                                         self._ws_bytes, self._status, tensors.current_stream_of(dev))
         if rc:
             raise capi.DecError(rc, "dec_pages_resize")
 
@@ -129,26 +129,26 @@ class PagedKV:
         """Sequence s becomes a copy of sequence parents[s] (int32; negative:
         empty), all at once, by sharing pages."""
         dev = self.device
-        if capi.elsewhere(dev, stream):
-            with capi.guard(dev, stream):
+        if tensors.elsewhere(dev, stream):
+            with tensors.guard(dev, stream):
                 return self.fork(parents)
-        capi.check_tensor(parents, "parents", torch.int32, (self.n_seqs,), dev)
+        tensors.check_tensor(parents, "parents", torch.int32, (self.n_seqs,), dev)
         rc = capi.lib().dec_pages_fork(*self._refs, parents.data_ptr(), self._status,
-                                       capi.current_stream_of(dev))
+                                       tensors.current_stream_of(dev))
         if rc:
             raise capi.DecError(rc, "dec_pages_fork")
 
     def compact(self, stream=None) -> torch.Tensor:
         """Live pages move to the lowest numbers; returns their count (int32 [1])."""
         dev = self.device
-        if capi.elsewhere(dev, stream):
-            with capi.guard(dev, stream):
+        if tensors.elsewhere(dev, stream):
+            with tensors.guard(dev, stream):
                 return self.compact()
         live = torch.empty(1, dtype=torch.int32, device=dev)
         ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
         rc = capi.lib().dec_pages_compact(*self._refs, live.data_ptr(), ws.data_ptr(),
                                           self._ws_bytes, self._status,
-                                          capi.current_stream_of(dev))
+                                          tensors.current_stream_of(dev))
         if rc:
             raise capi.DecError(rc, "dec_pages_compact")
         return live
@@ -164,24 +164,24 @@ class PagedKV:
         n_q_heads, head_dim] likewise into q_out (bf16; zeros if None), which
         is returned.  Tokens at negative positions are skipped."""
         dev = self.device
-        if capi.elsewhere(dev, stream):
-            with capi.guard(dev, stream):
+        if tensors.elsewhere(dev, stream):
+            with tensors.guard(dev, stream):
                 return self.append(layer, k, v, positions, seqs, rope, q, q_out, q_norm, k_norm, eps)
         D, H = self.head_dim, self.n_kv_heads
-        shape = check_heads(k, "k", dev)
+        shape = tensors.check_heads(k, "k", dev)
         T = shape[0]
-        if shape != (T, H, D) or check_heads(v, "v", dev) != shape or v.dtype != k.dtype:
+        if shape != (T, H, D) or tensors.check_heads(v, "v", dev) != shape or v.dtype != k.dtype:
             raise ValueError(f"k and v must be alike, [tokens, {H}, {D}]")
-        capi.check_tensor(positions, "positions", torch.int32, (T,), dev)
-        io = capi.dec_append(T, capi.dtype_code(k, "k"))
+        tensors.check_tensor(positions, "positions", torch.int32, (T,), dev)
+        io = capi.dec_append(T, tensors.dtype_code(k, "k"))
         if q is not None:
-            shape = check_heads(q, "q", dev)
+            shape = tensors.check_heads(q, "q", dev)
             if shape[0] != T or shape[2] != D or q.dtype != k.dtype:
                 raise ValueError(f"q must be [{T}, heads, {D}] of {k.dtype}")
             if q_out is None:
                 q_out = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
             else:
-                capi.check_tensor(q_out, "q_out", torch.bfloat16, shape, dev)
+                tensors.check_tensor(q_out, "q_out", torch.bfloat16, shape, dev)
             io.n_q_heads, io.q, io.q_stride = shape[1], q.data_ptr(), q.stride(0)
             io.q_out = q_out.data_ptr()
         elif q_out is not None:
@@ -189,20 +189,20 @@ class PagedKV:
         io.k, io.k_stride, io.v, io.v_stride = k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0)
         io.positions, io.eps = positions.data_ptr(), eps
         if seqs is not None:
-            capi.check_tensor(seqs, "seqs", torch.int32, (T,), dev)
+            tensors.check_tensor(seqs, "seqs", torch.int32, (T,), dev)
             io.seqs = seqs.data_ptr()
         if q_norm is not None:
-            capi.check_tensor(q_norm, "q_norm", torch.bfloat16, (D,), dev)
+            tensors.check_tensor(q_norm, "q_norm", torch.bfloat16, (D,), dev)
             io.q_norm = q_norm.data_ptr()
         if k_norm is not None:
-            capi.check_tensor(k_norm, "k_norm", torch.bfloat16, (D,), dev)
+            tensors.check_tensor(k_norm, "k_norm", torch.bfloat16, (D,), dev)
             io.k_norm = k_norm.data_ptr()
         if rope is not None:
             if rope.device != dev:
                 raise ValueError(f"rope must be on {dev}, got {rope.device}")
             io.rope = rope.pointer
         rc = capi.lib().dec_paged_append(*self._refs, layer, ctypes.byref(io), self._status,
-                                         capi.current_stream_of(dev))
+                                         tensors.current_stream_of(dev))
         if rc:
             raise capi.DecError(rc, "dec_paged_append")
         return q_out
@@ -216,18 +216,18 @@ class PagedKV:
         Returns out fp32 [batch, n_q_heads, head_dim], with return_lse also
         the log of the softmax sums [batch, n_q_heads]."""
         dev = self.device
-        if capi.elsewhere(dev, stream):
-            with capi.guard(dev, stream):
+        if tensors.elsewhere(dev, stream):
+            with tensors.guard(dev, stream):
                 return self.attend(layer, q, rows, window, out, return_lse)
-        B, Hq, D = shape = check_heads(q, "q", dev)
+        B, Hq, D = shape = tensors.check_heads(q, "q", dev)
         if q.dtype != torch.bfloat16 or D != self.head_dim:
             raise ValueError(f"q must be bfloat16 [batch, heads, {self.head_dim}]")
         if rows is not None:
-            capi.check_tensor(rows, "rows", torch.int32, (B,), dev)
+            tensors.check_tensor(rows, "rows", torch.int32, (B,), dev)
         if out is None:
             out = torch.empty(shape, dtype=torch.float32, device=dev)
         else:
-            capi.check_tensor(out, "out", torch.float32, shape, dev)
+            tensors.check_tensor(out, "out", torch.float32, shape, dev)
         nb = self._attend_bytes.get((B, Hq))
         if nb is None:
             nb = capi.dec_paged_attention_workspace_bytes(self.pool, B, Hq)
@@ -238,7 +238,7 @@ class PagedKV:
             *self._refs, layer, B, Hq, q.data_ptr(), q.stride(0),
             None if rows is None else rows.data_ptr(), window, out.data_ptr(),
             None if lse is None else lse.data_ptr(), ws.data_ptr(), nb, self._status,
-            capi.current_stream_of(dev))
+            tensors.current_stream_of(dev))
         if rc:
             raise capi.DecError(rc, "dec_paged_attention")
         return (out, lse) if return_lse else out

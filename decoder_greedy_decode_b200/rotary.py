@@ -11,7 +11,7 @@ from typing import Optional
 
 import torch
 
-from . import capi
+from . import capi, tensors
 
 SCALINGS = {"none": capi.DEC_ROPE_NONE, "linear": capi.DEC_ROPE_LINEAR,
             "ntk": capi.DEC_ROPE_NTK, "parts": capi.DEC_ROPE_PARTS}
@@ -52,28 +52,19 @@ class Rope:
         into `out` (which may be x).  The row of a token at a negative position
         is copied as it is."""
         dev = self.device
-        if capi.elsewhere(dev, stream):
-            with capi.guard(dev, stream):
+        if tensors.elsewhere(dev, stream):
+            with tensors.guard(dev, stream):
                 return self.apply(x, positions, out)
-        T, H, D = check_heads(x, "x", dev)
+        T, H, D = tensors.check_heads(x, "x", dev)
         if out is None:
             out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
-        elif out.dtype != x.dtype or check_heads(out, "out", dev) != (T, H, D):
+        elif out.dtype != x.dtype or tensors.check_heads(out, "out", dev) != (T, H, D):
             raise ValueError("out must have the shape and type of x")
-        capi.check_tensor(positions, "positions", torch.int32, (T,), dev)
-        rc = capi.lib().dec_rope_apply(T, H, D, capi.dtype_code(x, "x"), x.data_ptr(), x.stride(0),
+        tensors.check_tensor(positions, "positions", torch.int32, (T,), dev)
+        rc = capi.lib().dec_rope_apply(T, H, D, tensors.dtype_code(x, "x"), x.data_ptr(), x.stride(0),
                                        out.data_ptr(), out.stride(0), positions.data_ptr(),
-                                       self.pointer, capi.current_stream_of(dev))
+                                       self.pointer, tensors.current_stream_of(dev))
         if rc:
             raise capi.DecError(rc, "dec_rope_apply")
         return out
 
-
-def check_heads(t: torch.Tensor, name: str, device):
-    """The shape of a tensor [tokens, heads, head_dim] with contiguous heads."""
-    if t.dim() != 3 or t.device != device:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim] on {device}")
-    shape, stride = t.shape, t.stride()
-    if stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
-        raise ValueError(f"{name} must have contiguous heads, got strides {stride}")
-    return shape
