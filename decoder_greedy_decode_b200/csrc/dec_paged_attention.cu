@@ -17,8 +17,8 @@
 // tiles into a ring of the warp's own, several ahead and across sequence
 // boundaries, so no CTA barrier holds the stream up.  A run that covers a
 // whole sequence writes its output; otherwise it leaves its state in the
-// workspace and a second, dependent launch joins the states in run order (the
-// result does not depend on timing).  TMA does the copies: loads alone
+// workspace and, after a barrier of the grid, the states are joined in run
+// order (the result does not depend on timing).  TMA does the copies: loads alone
 // (nothing computed) ran at 7.0 TB/s so, and at 5.2 TB/s with per-lane
 // cp.async of the same rings (32 sequences of 16K to 32K rows).
 //
@@ -43,6 +43,7 @@
 // per head that keeps the largest p * scale near 2^14 (2^-22 relative, values
 // below 2^-39 of the largest lost).  q is made f16 by a power of two per
 // head, exact down to 2^-38 of the head's largest element.
+#include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -216,10 +217,10 @@ __device__ __forceinline__ void next(const PagedArgs& a, Place& p) {
 // Row of an octet that M index i stands for.
 __device__ __forceinline__ int row_of(int i) { return i ^ ((i & 1) << 2); }
 
+// This warp's run of tiles.
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) paged_kernel(
-    const PagedArgs a, const __grid_constant__ CUtensorMap kmap,
-    const __grid_constant__ CUtensorMap vmap) {
+__device__ __forceinline__ void run_tiles(const PagedArgs& a, const CUtensorMap& kmap,
+                                          const CUtensorMap& vmap) {
   using C = Cfg<D, FP8>;
   constexpr int S = C::S, NS = C::NS, TR = C::TR, ES = C::ES, HB = C::HB, TB = 2 * HB;
   constexpr int RB = D * ES < 128 ? D * ES : 128;  // bytes of a row in a box
@@ -231,7 +232,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) paged_kernel(
   constexpr int NO = TR / 8;                    // row octets of a tile
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t s_bar[kWarps][S];
-  __shared__ long long s_sum[kWarps];
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g8 = lane >> 2, t4 = lane & 3;
@@ -244,47 +244,49 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) paged_kernel(
     for (int i = 0; i < S; ++i) mbar_init(&s_bar[warp][i], 1);
     fence_mbar_init();
   }
-  pdl_trigger();
 
-  // The runs: all tiles, then this warp's first one.
+  // The runs: all tiles, then this warp's first one.  Every warp counts for
+  // itself; the lengths of the first 128 sequences are loaded once.
+  constexpr int R = 4;
+  int known[R];
   long long total = 0;
   {
-    long long sum = 0;
     int lo;
-    for (int b = threadIdx.x; b < a.B; b += kThreads) sum += tiles_of<TR>(a, a.rows[b], lo);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) s_sum[warp] = sum;
-    __syncthreads();
+    for (int c = 0; c < R; ++c) {
+      const int b = c * 32 + lane;
+      known[c] = b < a.B ? tiles_of<TR>(a, a.rows[b], lo) : 0;
+      total += known[c];
+    }
+    for (int b = R * 32 + lane; b < a.B; b += 32) total += tiles_of<TR>(a, a.rows[b], lo);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += s_sum[w];
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   }
   const long long run = (total + workers - 1) / workers;
   const long long first = worker * run;
   if (worker >= workers || first >= total) return;
   const int count = static_cast<int>(min(run, total - first));
-  // (each warp scans for itself: 32 sequences at a time)
-  long long base = 0;
+  long long base = 0;   // tiles before the sequence that holds the first one
   Place ip;
-  ip.b = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    int lo;
-    const int b = b0 + lane;
-    const long long n = b < a.B ? tiles_of<TR>(a, a.rows[b], lo) : 0;
-    long long inc = n;
+  ip.b = -1;
+  auto search = [&](int b0, int tiles) {   // among sequences b0 .. b0 + 31
+    long long upto = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += up;
+      const long long before = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += before;
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, base + inc > first);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      ip.b = b0 + l;
-      base += __shfl_sync(0xffffffffu, inc - n, l);
-      break;
-    }
-    base += __shfl_sync(0xffffffffu, inc, 31);
+    const unsigned hit = __ballot_sync(0xffffffffu, base + upto > first);
+    const int l = hit ? __ffs(hit) - 1 : 31;
+    base += __shfl_sync(0xffffffffu, hit ? upto - tiles : upto, l);
+    if (hit) ip.b = b0 + l;
+  };
+#pragma unroll
+  for (int c = 0; c < R; ++c)
+    if (ip.b < 0) search(c * 32, known[c]);
+  for (int b0 = R * 32; ip.b < 0 && b0 < a.B; b0 += 32) {
+    int lo;
+    search(b0, b0 + lane < a.B ? tiles_of<TR>(a, a.rows[b0 + lane], lo) : 0);
   }
   enter<TR>(a, ip);
   ip.tile = static_cast<int>(first - base);
@@ -301,49 +303,67 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) paged_kernel(
   auto fetch_ids = [&]() {
     const int r0 = row0<TR>(ip);
     const int32_t* row = a.table + static_cast<long long>(ip.b) * a.width;
+    if (BR == TR) {   // (the one box of a tile always holds rows)
+      ids[0] = row[r0 >> a.pool.shift];
+    } else {
 #pragma unroll
-    for (int o = 0; o < NO; ++o) {
-      const int r = r0 + BR * o;
-      ids[o] = (o * BR < TR && r + BR > ip.lo && r < ip.len) ? row[r >> a.pool.shift] : -2;
+      for (int o = 0; o < NO; ++o) {
+        const int r = r0 + BR * o;
+        ids[o] = (o * BR < TR && r + BR > ip.lo && r < ip.len) ? row[r >> a.pool.shift] : -2;
+      }
     }
   };
   int issued = 0;
   auto issue = [&]() {
     if (issued >= count) return;
     const int slot = issued % S;
+    auto outside = [&](int id) { return id < 0 || id >= a.pool.n_pages; };
     unsigned wrong = 0;
-    int boxes = 0;
+    int boxes = 1;
+    if (BR == TR) {
+      wrong = outside(ids[0]);
+    } else {
+      boxes = 0;
 #pragma unroll
-    for (int o = 0; o < NO; ++o)
-      if (ids[o] != -2) {
-        ++boxes;
-        if (ids[o] < 0 || ids[o] >= a.pool.n_pages) wrong = 1;
-      }
+      for (int o = 0; o < NO; ++o)
+        if (ids[o] != -2) {
+          ++boxes;
+          wrong |= outside(ids[o]);
+        }
+    }
     bad = (bad & ~(1u << slot)) | (wrong << slot);
     if (lane == 0) {
-      const uint32_t bar = smem_u32(&s_bar[warp][slot]);
+      uint64_t* bar = &s_bar[warp][slot];
       const uint32_t dst = ring + slot * TB, sdst = scales + slot * C::SB;
       constexpr int row_total = 2 * D * ES + (FP8 ? 8 : 0);   // bytes of a K and V row
+      const int y = (g << a.pool.shift) + (row0<TR>(ip) & (P - 1));
+      // boxes of one tile lie in different pages, at the same rows of them
+      auto box = [&](int o, int page) {
+        const uint32_t at = dst + o * BR * RB;
+#pragma unroll
+        for (int h = 0; h < NB; ++h) {
+          load_box(at + h * (TR * RB), &kmap, h * 64, y, page, smem_u32(bar), policy);
+          load_box(at + HB + h * (TR * RB), &vmap, h * 64, y, page, smem_u32(bar), policy);
+        }
+        if constexpr (FP8) {
+          const long long e = page * (a.pool.page_stride / D) + y;
+          bulk_u32(sdst + o * BR * 4, a.pool.ks + e, BR * 4, smem_u32(bar), policy);
+          bulk_u32(sdst + (TR + o * BR) * 4, a.pool.vs + e, BR * 4, smem_u32(bar), policy);
+        }
+      };
       if (wrong) {
-        mbar_arrive(&s_bar[warp][slot]);
+        mbar_arrive(bar);
+      } else if (BR == TR) {
+        mbar_arrive_expect_tx(bar, TR * row_total);
+        box(0, ids[0]);
       } else {
-        mbar_arrive_expect_tx(&s_bar[warp][slot], boxes * BR * row_total);
-        const int y = (g << a.pool.shift) + (row0<TR>(ip) & (P - 1));
+        mbar_arrive_expect_tx(bar, boxes * BR * row_total);
+#pragma unroll 1
+        for (int o = 0; o * BR < TR; ++o) {
+          int page = ids[0];
 #pragma unroll
-        for (int o = 0; o < NO; ++o) {
-          if (ids[o] == -2) continue;
-          // (boxes of one tile lie in different pages: at the same rows of them)
-          const uint32_t at = dst + o * BR * RB;
-#pragma unroll
-          for (int h = 0; h < NB; ++h) {
-            load_box(at + h * (TR * RB), &kmap, h * 64, y, ids[o], bar, policy);
-            load_box(at + HB + h * (TR * RB), &vmap, h * 64, y, ids[o], bar, policy);
-          }
-          if constexpr (FP8) {
-            const long long e = ids[o] * (a.pool.page_stride / D) + y;
-            bulk_u32(sdst + o * BR * 4, a.pool.ks + e, BR * 4, bar, policy);
-            bulk_u32(sdst + (TR + o * BR) * 4, a.pool.vs + e, BR * 4, bar, policy);
-          }
+          for (int k = 1; k < NO; ++k) page = o == k ? ids[k] : page;
+          if (page != -2) box(o, page);
         }
       }
     }
@@ -770,74 +790,155 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) paged_kernel(
 }
 
 // Joins the states of one (sequence, query head); also the outputs of empty
-// sequences.  The states' weights come first, so that the sums' loads are
-// independent: four groups of 32 lanes take every fourth state.
+// sequences.  A warp takes up to 32 states (a lane each for the weights);
+// sequences that more workers share are joined by their CTA.  The weights come
+// first, so that the loads of the sums are independent.
+struct Item {
+  int2 d;          // first worker, workers (0: nothing to join)
+  int g, hh;       // KV head, query head of its group
+  float *out, *lse;
+};
 template <int D>
-__global__ void __launch_bounds__(128) join_kernel(const PagedArgs a) {
-  extern __shared__ float s_w[];   // [states]
-  __shared__ float s_acc[4][D];
-  __shared__ float s_red[4];
-  const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq;
-  const int g = h / a.rep, hh = h % a.rep;
-  const int tid = threadIdx.x, grp = tid >> 5, lane = tid & 31;
-  pdl_wait();
-  const int2 d = a.desc[b];   // (of no use for an empty sequence)
+__device__ __forceinline__ Item item_at(const PagedArgs& a, int item, bool first_lane) {
+  const int b = item / a.Hq, h = item % a.Hq;
+  Item it{make_int2(0, 0), h / a.rep, h % a.rep, a.out + static_cast<long long>(item) * D,
+          a.lse ? a.lse + item : nullptr};
+  const int2 d = __ldcg(&a.desc[b]);   // (of no use for an empty sequence)
   const int n = a.rows[b];
-  float* out = a.out + (static_cast<long long>(b) * a.Hq + h) * D;
-  float* lse = a.lse ? a.lse + static_cast<long long>(b) * a.Hq + h : nullptr;
   if (n < 0 || n > a.max_rows) {
-    if (tid == 0 && h == 0 && a.status) atomicOr(a.status, DEC_DEV_BAD_POSITION);
-    return;
+    if (first_lane && h == 0 && a.status) atomicOr(a.status, DEC_DEV_BAD_POSITION);
+  } else if (n == 0) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) it.out[e * 32 + lane] = 0.f;
+    if (first_lane && it.lse) *it.lse = -INFINITY;
+  } else {
+    it.d = d;
   }
-  if (n == 0) {
-    if (tid < D) out[tid] = 0.f;
-    if (tid == 0 && lse) *lse = -INFINITY;
-    return;
+  return it;
+}
+// State i: the first is its warp's last, the others their warps' first.
+__device__ __forceinline__ const float* state_of(const PagedArgs& a, const Item& it, int D, int i) {
+  const int words = a.rep * (D + 2);
+  return a.part + (static_cast<long long>(it.d.x + i) * a.Hkv + it.g) * (2 * words) + (i == 0 ? words : 0);
+}
+template <int D>
+__device__ __forceinline__ void join_by_warp(const PagedArgs& a, const Item& it) {
+  const int lane = threadIdx.x & 31, n = it.d.y;
+  float m = -INFINITY, l = 0.f;
+  if (lane < n) {
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(state_of(a, it, D, lane) + a.rep * D) + it.hh);
+    m = ml.x;
+    l = ml.y;
   }
-  if (d.y == 0) return;   // written by its one warp
-  const int rep = a.rep, words = rep * (D + 2);
-  // the first state is its warp's last, the others their warps' first
-  auto state = [&](int i) {
-    return a.part + (static_cast<long long>(d.x + i) * a.Hkv + g) * (2 * words) + (i == 0 ? words : 0);
-  };
+  if (__any_sync(0xffffffffu, m != m)) return;   // poisoned
+  const float M = warp_max(m);
+  const float w = m == -INFINITY ? 0.f : ex2(m - M);
+  l = warp_sum(l * w);
+  float acc[D / 32];
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float* v = state_of(a, it, D, i) + it.hh * D + lane;
+    const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(__ldcg(v + 32 * e), wi, acc[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) it.out[e * 32 + lane] = acc[e] / l;
+  if (lane == 0 && it.lse) *it.lse = (M + log2f(l)) * 0.6931471805599453f;
+}
+// s_w: a float per worker; every thread of the CTA.
+template <int D>
+__device__ __forceinline__ void join_by_cta(const PagedArgs& a, const Item& it, float* s_w) {
+  __shared__ float s_acc[kWarps][D];
+  __shared__ float s_red[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = it.d.y;
   float m = -INFINITY;
   bool poison = false;
-  for (int i = tid; i < d.y; i += 128) {
-    const float v = __ldcg(state(i) + rep * D + 2 * hh);
+  for (int i = tid; i < n; i += kThreads) {
+    const float v = __ldcg(state_of(a, it, D, i) + a.rep * D + 2 * it.hh);
     s_w[i] = v;
     poison |= v != v;
     m = fmaxf(m, v);
   }
   m = warp_max(m);
-  if (lane == 0) s_red[grp] = m;
+  if (lane == 0) s_red[warp] = m;
   if (__syncthreads_or(poison)) return;
-  m = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_red[w]);
   float l = 0.f;
-  for (int i = tid; i < d.y; i += 128) {
+  for (int i = tid; i < n; i += kThreads) {
     const float w = s_w[i] == -INFINITY ? 0.f : ex2(s_w[i] - m);
-    l += __ldcg(state(i) + rep * D + 2 * hh + 1) * w;
+    l += __ldcg(state_of(a, it, D, i) + a.rep * D + 2 * it.hh + 1) * w;
     s_w[i] = w;
   }
   l = warp_sum(l);
   __syncthreads();   // s_red has been read, s_w is complete
-  if (lane == 0) s_red[grp] = l;
-  constexpr int E = D / 32;
-  float acc[E];
+  if (lane == 0) s_red[warp] = l;
+  float acc[D / 32];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
 #pragma unroll 4
-  for (int i = grp; i < d.y; i += 4) {
-    const float* v = state(i) + hh * D + lane;
+  for (int i = warp; i < n; i += kWarps) {
+    const float* v = state_of(a, it, D, i) + it.hh * D + lane;
     const float w = s_w[i];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(__ldcg(v + 32 * e), w, acc[e]);
+    for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(__ldcg(v + 32 * e), w, acc[e]);
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_acc[grp][e * 32 + lane] = acc[e];
+  for (int e = 0; e < D / 32; ++e) s_acc[warp][e * 32 + lane] = acc[e];
   __syncthreads();
-  l = s_red[0] + s_red[1] + s_red[2] + s_red[3];
-  if (tid < D) out[tid] = (s_acc[0][tid] + s_acc[1][tid] + s_acc[2][tid] + s_acc[3][tid]) / l;
-  if (tid == 0 && lse) *lse = (m + log2f(l)) * 0.6931471805599453f;
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) l += s_red[w];
+  for (int e = tid; e < D; e += kThreads) {
+    float x = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) x += s_acc[w][e];
+    it.out[e] = x / l;
+  }
+  if (tid == 0 && it.lse) *it.lse = (m + log2f(l)) * 0.6931471805599453f;
+  __syncthreads();   // before the shared arrays are used again
+}
+
+// One cooperative launch: all runs, a barrier of the grid, the joins.  (As two
+// launches, the second one dependent, the host's part of a call was 9.1 us
+// against 4.6, and the GPU's the same.)
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) paged_kernel(
+    const PagedArgs a, const __grid_constant__ CUtensorMap kmap,
+    const __grid_constant__ CUtensorMap vmap) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Item s_many[kWarps];
+  __shared__ int s_n;
+  if (threadIdx.x == 0) s_n = 0;
+  run_tiles<D, FP8>(a, kmap, vmap);
+  cooperative_groups::this_grid().sync();
+  const int lane = threadIdx.x & 31;
+  const long long items = static_cast<long long>(a.B) * a.Hq;
+  const int hop = gridDim.x * kWarps;
+  for (long long base = 0; base < items; base += hop) {
+    // neighbouring items on different SMs
+    const long long item = base + (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+    if (item < items) {
+      const Item it = item_at<D>(a, static_cast<int>(item), lane == 0);
+      if (it.d.y > 32) {
+        if (lane == 0) s_many[atomicAdd(&s_n, 1)] = it;
+      } else if (it.d.y > 0) {
+        join_by_warp<D>(a, it);
+      }
+    }
+    __syncthreads();
+    const int n = s_n;
+    for (int i = 0; i < n; ++i) join_by_cta<D>(a, s_many[i], reinterpret_cast<float*>(smem_raw));
+    if (n) {   // (join_by_cta may end early for a poisoned sequence)
+      __syncthreads();
+      if (threadIdx.x == 0) s_n = 0;
+    }
+    __syncthreads();
+  }
 }
 
 template <int D, bool FP8>
@@ -847,12 +948,17 @@ cudaError_t launch_paged(const PagedArgs& a, const CUtensorMap& km, const CUtens
   constexpr int smem = Cfg<D, FP8>::SMEM;
   cudaError_t e = allow_smem(paged_kernel<D, FP8>, smem, done);
   if (e != cudaSuccess) return e;
-  paged_kernel<D, FP8><<<grid, kThreads, smem, s>>>(a, km, vm);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const size_t states = sizeof(float) * kWarps * grid / a.Hkv;   // at most a worker's each
-  return launch_dependent(join_kernel<D>, dim3(static_cast<unsigned>(a.B) * a.Hq), dim3(128), states,
-                          s, a);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeCooperative;
+  at[0].val.cooperative = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_kernel<D, FP8>, a, km, vm);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,

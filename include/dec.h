@@ -649,8 +649,8 @@ size_t dec_paged_attention_workspace_bytes(const dec_pages *pool, int batch, int
  * their mix.  rows[b] < 0 or behind the table's end raises
  * DEC_DEV_BAD_POSITION, an unassigned page DEC_DEV_BAD_PAGE; that sequence's
  * outputs (of the KV heads concerned) are left as they were.  map->refs is
- * not used.  Asynchronous on `stream` (two launches, the second one
- * dependent). */
+ * not used.  Asynchronous on `stream` (one cooperative launch of a grid that
+ * fills the GPU). */
 int dec_paged_attention(const dec_pages *pool, const dec_page_map *map, int layer, int batch,
                         int n_q_heads, const void *q, long long q_stride, const int32_t *rows,
                         int window, float *out, float *lse, void *workspace,
