@@ -329,45 +329,81 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const BeamArgs a) {
   }
 }
 
-// One CTA per group.  A warp joins a row: its sum, and its k best keys from
-// the chunks' sorted lists (a lane holds the heads of up to four lists).
-__global__ void __launch_bounds__(kThreads) groups_kernel(const BeamArgs a) {
+// The k best of a row from the sorted lists of its chunks, by one warp: a lane
+// holds the heads (and the next keys) of NL lists.
+template <int NL>
+__device__ __forceinline__ void merge_lists(const BeamArgs& a, const unsigned long long* lists,
+                                            double own, double lse, uint32_t row0, double* sc,
+                                            uint32_t* at, const unsigned long long (&first)[4],
+                                            const unsigned long long (&second)[4]) {
+  const int lane = threadIdx.x & 31;
+  unsigned long long head[NL], then[NL];
+  int pos[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    head[i] = first[i];
+    then[i] = second[i];
+    pos[i] = 2;
+  }
+  for (int p = 0; p < a.k; ++p) {
+    unsigned long long mine = head[0];
+#pragma unroll
+    for (int i = 1; i < NL; ++i) mine = max(mine, head[i]);
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(mine >> 32));
+    const uint32_t lo = __reduce_max_sync(
+        0xffffffffu, static_cast<uint32_t>(mine >> 32) == hi ? static_cast<uint32_t>(mine) : 0u);
+    const unsigned long long best = (static_cast<unsigned long long>(hi) << 32) | lo;
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      if (head[i] == best) {   // (keys are unique; a row holds at least k)
+        head[i] = then[i];
+        then[i] = pos[i] < a.k ? __ldcg(lists + (i * 32 + lane) * a.k + pos[i]) : 0ull;
+        ++pos[i];
+      }
+    if (lane == 0) {
+      const double v = own + static_cast<double>(logit_of(best)) - lse;
+      sc[p] = v == v ? v : -INFINITY;
+      at[p] = row0 + static_cast<uint32_t>(~lo);
+    }
+  }
+}
+
+// One CTA per group, a warp per row: its sum, and its k best keys.
+__global__ void __launch_bounds__(kMaxBeams * 32) groups_kernel(const BeamArgs a) {
   __shared__ double s_score[kMaxBeams * kMaxK];
   __shared__ uint32_t s_at[kMaxBeams * kMaxK];
   __shared__ bool s_done[kMaxBeams];   // (out_done may be done)
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int g = blockIdx.x;
-  const double ninf = -INFINITY;
   pdl_wait();
-  for (int w = warp; w < a.W; w += kThreads / 32) {
+  if (w < a.W) {
     const long long r = static_cast<long long>(g) * a.W + w;
     // (loads first: the lists' heads do not wait for the row's sum)
     const unsigned long long* lists = a.key + r * a.chunks * a.k;
-    unsigned long long head[kMaxLists / 32], then[kMaxLists / 32];
-    int pos[kMaxLists / 32];
     const double own = a.scores[r];
     const bool done = a.done && a.done[r];
     if (lane == 0) s_done[w] = done;
+    unsigned long long first[kMaxLists / 32], second[kMaxLists / 32];
+    float2 t[kMaxLists / 32];
 #pragma unroll
     for (int i = 0; i < kMaxLists / 32; ++i) {
       const int c = i * 32 + lane;
       const bool has = !done && c < a.chunks;
-      head[i] = has ? __ldcg(lists + c * a.k) : 0ull;
-      then[i] = has && a.k > 1 ? __ldcg(lists + c * a.k + 1) : 0ull;
-      pos[i] = 2;
+      first[i] = has ? __ldcg(lists + c * a.k) : 0ull;
+      second[i] = has && a.k > 1 ? __ldcg(lists + c * a.k + 1) : 0ull;
+      t[i] = has ? __ldcg(&a.stat[r * a.chunks + c]) : make_float2(-INFINITY, 0.f);
     }
-    bool flat = !(own > ninf);   // -inf or NaN: no candidate above -inf
+    bool flat = !(own > -INFINITY);   // -inf or NaN: no candidate above -inf
     double lse = 0.0;
     if (!done && !flat) {
       float M = -INFINITY;
-      for (int c = lane; c < a.chunks; c += 32) M = fmaxf(M, __ldcg(&a.stat[r * a.chunks + c]).x);
+#pragma unroll
+      for (int i = 0; i < kMaxLists / 32; ++i) M = fmaxf(M, t[i].x);
       M = warp_max(M);
       double sum = 0.0;
-      for (int c = lane; c < a.chunks; c += 32) {
-        const float2 t = __ldcg(&a.stat[r * a.chunks + c]);
-        sum += static_cast<double>(t.y) *
-               static_cast<double>(t.x == -INFINITY ? 1.f : ex2((t.x - M) * kLog2e));
-      }
+#pragma unroll
+      for (int i = 0; i < kMaxLists / 32; ++i)
+        sum += static_cast<double>(t[i].x == -INFINITY ? t[i].y : t[i].y * ex2((t[i].x - M) * kLog2e));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       lse = static_cast<double>(M) + log(sum);
@@ -380,55 +416,36 @@ __global__ void __launch_bounds__(kThreads) groups_kernel(const BeamArgs a) {
     if (flat || done) {
       for (int p = lane; p < a.k; p += 32) {
         if (flat) {
-          sc[p] = ninf;
+          sc[p] = -INFINITY;
           at[p] = row0 + p;
         } else if (p == 0) {
           sc[0] = own;
           at[0] = row0 + a.eos;
         } else {
-          sc[p] = ninf;
+          sc[p] = -INFINITY;
           at[p] = row0 + (p - 1 < a.eos ? p - 1 : p);
         }
       }
-      continue;
-    }
-    for (int p = 0; p < a.k; ++p) {
-      unsigned long long best = head[0];
-#pragma unroll
-      for (int i = 1; i < kMaxLists / 32; ++i) best = head[i] > best ? head[i] : best;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const unsigned long long other = __shfl_xor_sync(0xffffffffu, best, o);
-        best = other > best ? other : best;
-      }
-#pragma unroll
-      for (int i = 0; i < kMaxLists / 32; ++i)
-        if (head[i] == best && best) {
-          head[i] = then[i];
-          then[i] = pos[i] < a.k ? __ldcg(lists + (i * 32 + lane) * a.k + pos[i]) : 0ull;
-          ++pos[i];
-        }
-      if (lane == 0) {
-        const double v = own + static_cast<double>(logit_of(best)) - lse;
-        sc[p] = v == v ? v : ninf;
-        at[p] = row0 + static_cast<uint32_t>(~static_cast<uint32_t>(best));
-      }
+    } else if (a.chunks <= 32) {
+      merge_lists<1>(a, lists, own, lse, row0, sc, at, first, second);
+    } else {
+      merge_lists<kMaxLists / 32>(a, lists, own, lse, row0, sc, at, first, second);
     }
   }
   __syncthreads();
   const int n = a.W * a.k;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
     const double v = s_score[i];
     const uint32_t at = s_at[i];
     int rank = 0;
     for (int j = 0; j < n; ++j) rank += s_score[j] > v || (s_score[j] == v && s_at[j] < at);
     if (rank >= a.k) continue;
     const long long o = static_cast<long long>(g) * a.k + rank;
-    const int w = at / a.V, t = at % a.V;
+    const int beam = at / a.V, token = at % a.V;
     a.out_scores[o] = static_cast<float>(v);
-    a.out_parents[o] = w;
-    a.out_tokens[o] = t;
-    if (a.out_done) a.out_done[o] = s_done[w] || t == a.eos;
+    a.out_parents[o] = beam;
+    a.out_tokens[o] = token;
+    if (a.out_done) a.out_done[o] = s_done[beam] || token == a.eos;
   }
 }
 
@@ -538,8 +555,8 @@ struct Plan {
 Plan plan_of(int rows, int V, int k, int sms) {
   Plan p{};
   const int len = V + 7;   // and the elements before the first 16-byte boundary
-  int want = (4 * sms + rows - 1) / rows;
-  want = want > kMaxLists ? kMaxLists : want;
+  int want = 4 * sms / rows;
+  want = want < 1 ? 1 : want > kMaxLists ? kMaxLists : want;
   p.chunk = ((len + want - 1) / want + kBatch / 2 - 1) / (kBatch / 2) * (kBatch / 2);
   p.chunks = (len + p.chunk - 1) / p.chunk;
   p.stat = round256(sizeof(float2) * static_cast<size_t>(rows) * p.chunks);
@@ -612,7 +629,7 @@ extern "C" int dec_beam_select(int groups, int beams, int vocab, int k, int dtyp
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   e = dtype == DEC_BF16 ? launch_beam_rows<uint16_t>(a, s) : launch_beam_rows<float>(a, s);
-  if (e == cudaSuccess) e = launch_dependent(groups_kernel, dim3(groups), dim3(kThreads), 0, s, a);
+  if (e == cudaSuccess) e = launch_dependent(groups_kernel, dim3(groups), dim3(32 * beams), 0, s, a);
   return e == cudaSuccess ? DEC_OK : cuda_failed(e);
 }
 
