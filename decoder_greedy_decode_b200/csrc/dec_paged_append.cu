@@ -7,7 +7,7 @@
 // 2^-33 turns (a product in fp32 is off by p * f_i * 2^-24 radians, i.e. by
 // 0.06 rad at p = 2^20).  The rotation itself is fp32, rounded once.
 //
-// Split.  A warp takes one token and some of its head rows, four at a time:
+// Split.  A warp takes tokens, and the head rows of each four at a time:
 // eight lanes hold a row, 16 (head_dim 128) or 8 (64) of its elements each, so
 // loads and stores are 16 bytes a lane and one three-step butterfly reduces
 // four rows (RMSNorm sums, E4M3 maxima).  Nothing passes through shared
@@ -215,7 +215,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
   constexpr int N = D / 16;     // pairs of a lane
   constexpr int V = vector_of<T, D>(), K = 2 * N / V;
   const int lane = threadIdx.x & 31, oct = lane >> 3, o = lane & 7;
-  const int rows = a.Hq + 2 * a.Hkv, quads = (rows + 3) / 4;
+  // quads of q, k and v rows in this order: a quad is all of one kind, so what
+  // it passes through is uniform (idle octets where heads are no multiple of 4)
+  const int nq = (a.Hq + 3) / 4, nk = (a.Hkv + 3) / 4, quads = nq + 2 * nk;
   const int r = a.rot >> 1;
   // A job is a token's quads part, part + per_token, ...; a warp takes jobs
   // `hop` apart.
@@ -223,24 +225,32 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
   const int job0 = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (job0 >= jobs) return;
 
-  // section of a row: 0 q, 1 k, 2 v
-  auto section = [&](int i) { return i < a.Hq ? 0 : i < a.Hq + a.Hkv ? 1 : 2; };
-  // (rows that are not rotated are read as neighbours in every mode)
-  auto source = [&](int t, int i, int sec) {
-    return sec == 0   ? static_cast<const T*>(a.q) + t * a.q_stride + i * D
-           : sec == 1 ? static_cast<const T*>(a.k) + t * a.k_stride + (i - a.Hq) * D
-                      : static_cast<const T*>(a.v) + t * a.v_stride + (i - a.Hq - a.Hkv) * D;
+  // kind of a quad: 0 q, 1 k, 2 v; this octet's head (an idle one's: the last)
+  auto kind_of = [&](int quad) { return quad < nq ? 0 : quad < nq + nk ? 1 : 2; };
+  auto head_of = [&](int quad, int kind) {
+    return 4 * (quad - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) + oct;
   };
-  auto split = [&](int sec) { return M != kPairs && a.phases && sec < 2; };
+  auto source = [&](int t, int kind, int head) {
+    const void* base = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+    const long long stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
+    return static_cast<const T*>(base) + t * stride + min(head, (kind == 0 ? a.Hq : a.Hkv) - 1) * D;
+  };
+  // where the lane's runs start in rows that are rotated, and in others
+  // (neighbours in every mode)
+  int split_at[K], plain_at[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    plain_at[k] = run_at<D, V>(false, k, o, a.rot);
+    split_at[k] = M == kPairs || !a.phases ? plain_at[k] : run_at<D, V>(true, k, o, a.rot);
+  }
   Raw<T, V> raw[K];   // the next quad, across the tokens of a warp
   int fjob = job0, ft = job0 / per_token, fquad = job0 % per_token;   // next quad to load
   auto fetch = [&]() {
     if (M == kScalar || fjob >= jobs) return;
-    // (behind the last row: the last one again, never written)
-    const int i = min(4 * fquad + oct, rows - 1), sec = section(i);
-    const T* p = source(ft, i, sec);
+    const int kind = kind_of(fquad);
+    const T* p = source(ft, kind, head_of(fquad, kind));
 #pragma unroll
-    for (int k = 0; k < K; ++k) raw[k].load(p + run_at<D, V>(split(sec), k, o, a.rot));
+    for (int k = 0; k < K; ++k) raw[k].load(p + (kind < 2 ? split_at[k] : plain_at[k]));
     fquad += per_token;
     if (fquad >= quads) {
       fjob += hop;
@@ -283,9 +293,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
     const int p = pair_at<D, V>(M != kPairs, oct * (N / 4) + j, o);
     phase[j] = a.phases && p < r ? a.phases[p] : 0;
   }
-  uint32_t g[N];                   // the gains of section `gains`, bf16 pairs
-  int gains = -1;
-
 #pragma unroll 1
   for (int job = job0; job < jobs; job += hop) {
   const int t = job / per_token, part = job % per_token;
@@ -337,9 +344,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
       }
     }
   }
-  // element of a row that x[i] is
-  auto element = [&](bool half, int i) {
-    if (M != kScalar || !half) return run_at<D, V>(half, i / V, o, a.rot) + i % V;
+  // element of a rotated row that x[i] is, one by one
+  auto element = [&](int i) {
     const int p = pair_at<D, V>(true, i % N, o);
     return i < N ? first_of<D>(p, a.rot) : second_of<D>(p, a.rot);
   };
@@ -351,41 +357,42 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
   const bool whole = 2 * r == D;   // every pair turns
 
 #pragma unroll 1
-  for (int base = 4 * part; base < rows; base += 4 * per_token) {   // rows base .. base + 3
-    const int row = base + oct;
-    const bool live = keep && row < rows;
-    const int sec = section(min(row, rows - 1));
-    const int least = section(base), most = section(min(base + 3, rows - 1));   // of the four
-    const bool half = split(sec);
+  for (int quad = part; quad < quads; quad += per_token) {
+    const int kind = kind_of(quad), head = head_of(quad, kind);
+    const bool live = keep && head < (kind == 0 ? a.Hq : a.Hkv);
+    const bool loose = M == kScalar && kind < 2 && a.phases;   // element by element
     float x[2 * N];
     if constexpr (M != kScalar) {
 #pragma unroll
       for (int k = 0; k < K; ++k) raw[k].get(x + k * V);
       fetch();
     } else {
-      const T* p = source(t, min(row, rows - 1), sec);
+      const T* p = source(t, kind, head);
 #pragma unroll
-      for (int i = 0; i < 2 * N; ++i) x[i] = ld1(p + element(half, i));
+      for (int i = 0; i < 2 * N; ++i) x[i] = ld1(p + (loose ? element(i) : plain_at[i / V] + i % V));
     }
-    if (least < 2 && (a.q_norm || a.k_norm)) {
+    const uint16_t* gain = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
+    if (gain) {
+      float g[2 * N];
+      if (loose) {
+#pragma unroll
+        for (int i = 0; i < 2 * N; ++i) g[i] = ld1(gain + element(i));
+      } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          Raw<uint16_t, V> w;
+          w.load(gain + split_at[k]);
+          w.get(g + k * V);
+        }
+      }
       float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < N; ++i) ss = fma2(pair(x, i), pair(x, i), ss);
       const float f = rsqrtf(row_sum(ss.x + ss.y) * (1.0f / D) + a.eps);
-      const uint16_t* gain = sec == 0 ? a.q_norm : sec == 1 ? a.k_norm : nullptr;
-      if (gain) {
-        if (gains != sec) {
-          gains = sec;
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-            g[i] = pack_bf16x2(gain[element(half, 2 * i)], gain[element(half, 2 * i + 1)]);
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          set(x, i, mul2(mul2(pair(x, i), make_float2(f, f)), make_float2(bf16lo(g[i]), bf16hi(g[i]))));
-      }
+      for (int i = 0; i < N; ++i) set(x, i, mul2(mul2(pair(x, i), make_float2(f, f)), pair(g, i)));
     }
-    if (turned && sec < 2) {
+    if (turned && kind < 2) {
       // a passed pair is not multiplied (cosine 1 and sine 0 would turn an
       // infinity in it into NaN)
 #pragma unroll
@@ -410,22 +417,27 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
       }
     }
     auto write = [&](auto* p) {
-      using E = typename std::remove_pointer<decltype(p)>::type;
-      if (M != kScalar || !half) {
+      if (loose) {
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-          put<V>(static_cast<E*>(p + run_at<D, V>(half, k, o, a.rot)), x + k * V);
+        for (int i = 0; i < 2 * N; ++i) put1(p + element(i), x[i]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 2 * N; ++i) put1(static_cast<E*>(p + element(half, i)), x[i]);
+        for (int k = 0; k < K; ++k) put<V>(p + (kind < 2 ? split_at[k] : plain_at[k]), x + k * V);
       }
     };
-    if (CACHE == 2 && most > 0) {
-      float am = 0.f;
+    if (kind == 0) {
+      if (live) write(static_cast<TO*>(a.q_out) + t * a.q_out_stride + head * D);
+      continue;
+    }
+    if constexpr (CACHE > 0) {
+      const long long e = row0 + (static_cast<long long>(head) << a.pool.shift) * D;
+      if constexpr (CACHE == 1) {
+        if (live) write(reinterpret_cast<uint16_t*>(kind == 1 ? a.pool.k : a.pool.v) + e);
+      } else {
+        float am = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2 * N; ++i) am = fmaxf(am, fabsf(x[i]));
-      am = fmaxf(row_max(am), 1.17549435e-38f);  // 2^-126
-      if (live && sec > 0) {
+        for (int i = 0; i < 2 * N; ++i) am = fmaxf(am, fabsf(x[i]));
+        am = fmaxf(row_max(am), 1.17549435e-38f);  // 2^-126
         float sc, den;   // the scale, and the scale times a power of two
         if (am >= 0x1p-60f && am <= 0x1p100f) {
           constexpr float y = 1.0f / 448.0f;
@@ -448,18 +460,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
           const float2 q = fma2(fma2(q0, neg2, v), inv2, q0);
           set(x, i, make_float2(copysignf(q.x, v.x), copysignf(q.y, v.y)));   // (-0 stays -0)
         }
-        const long long e =
-            row0 + (static_cast<long long>(row - (sec == 1 ? a.Hq : a.Hq + a.Hkv)) << a.pool.shift) * D;
-        write((sec == 1 ? a.pool.k : a.pool.v) + e);
-        if (o == 0) (sec == 1 ? a.pool.ks : a.pool.vs)[e / D] = sc;
+        if (live) {
+          write((kind == 1 ? a.pool.k : a.pool.v) + e);
+          if (o == 0) (kind == 1 ? a.pool.ks : a.pool.vs)[e / D] = sc;
+        }
       }
-    }
-    if (live && sec == 0)
-      write(static_cast<TO*>(a.q_out) + t * a.q_out_stride + static_cast<long long>(row) * D);
-    if (CACHE == 1 && live && sec > 0) {
-      const long long e =
-          row0 + (static_cast<long long>(row - (sec == 1 ? a.Hq : a.Hq + a.Hkv)) << a.pool.shift) * D;
-      write(reinterpret_cast<uint16_t*>(sec == 1 ? a.pool.k : a.pool.v) + e);
     }
   }
   }
@@ -470,7 +475,7 @@ cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t s) {
   // Warps of a token: one when the tokens alone give every SM its warps (the
   // angles are then computed once a token), up to one for four rows when
   // there are few tokens and latency counts.
-  const int most = (a.Hq + 2 * a.Hkv + 3) / 4;
+  const int most = (a.Hq + 3) / 4 + 2 * ((a.Hkv + 3) / 4);
   const long long want = (32ll * sms + a.n_tokens - 1) / a.n_tokens;
   const int per_token = static_cast<int>(want < 1 ? 1 : want > most ? most : want);
   const long long jobs = static_cast<long long>(a.n_tokens) * per_token;
@@ -597,7 +602,7 @@ extern "C" int dec_paged_append(const dec_pages* pool, const dec_page_map* map, 
   if (!is_aligned(io->k, 16) || !is_aligned(io->v, 16)) return DEC_ERR_ALIGN;
   if (io->n_q_heads && (!is_aligned(io->q, 16) || !is_aligned(io->q_out, 16)))
     return DEC_ERR_ALIGN;
-  if ((io->q_norm && !is_aligned(io->q_norm, 2)) || (io->k_norm && !is_aligned(io->k_norm, 2)))
+  if ((io->q_norm && !is_aligned(io->q_norm, 16)) || (io->k_norm && !is_aligned(io->k_norm, 16)))
     return DEC_ERR_ALIGN;
   if ((rc = check_stride(io->k_stride, n, pool->n_kv_heads, D)) != DEC_OK) return rc;
   if ((rc = check_stride(io->v_stride, n, pool->n_kv_heads, D)) != DEC_OK) return rc;

@@ -607,7 +607,8 @@ typedef struct dec_append {
   const int32_t *positions;   /* [n_tokens] row each token is written to;
                                * negative = padding, skipped whole */
   const int32_t *seqs;        /* [n_tokens] its sequence; NULL: token i is sequence i */
-  const void *q_norm, *k_norm;/* bf16 [head_dim] RMSNorm gains, or NULL for none */
+  const void *q_norm, *k_norm;/* bf16 [head_dim] RMSNorm gains (16-byte aligned),
+                               * or NULL for none */
   float eps;
   const dec_rope *rope;       /* HOST struct, or NULL for no rotation */
 } dec_append;

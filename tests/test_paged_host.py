@@ -117,7 +117,7 @@ def test_append_refuses_bad_arguments():
     assert go(q=None) == -1 and go(q_out=None) == -1 and go(n_q_heads=0) == -1
     assert go(eps=-1.0) == -9 and go(eps=float("nan")) == -9
     assert go(k=P + 4) == -6 and go(q=P + 2) == -6 and go(q_out=P + 4) == -6
-    assert go(dtype=1, v=P + 8) == -6 and go(q_norm=P + 1) == -6
+    assert go(dtype=1, v=P + 8) == -6 and go(q_norm=P + 8) == -6
     assert go(k_stride=4100) == -6 and go(k_stride=512) == -2 and go(q_stride=2040) == -2
     for rope, code in ((capi.dec_rope(None, 128, 0, 1.0), -1), (capi.dec_rope(P, 0, 0, 1.0), -2),
                        (capi.dec_rope(P, 130, 0, 1.0), -2), (capi.dec_rope(P, 7, 0, 1.0), -2),
