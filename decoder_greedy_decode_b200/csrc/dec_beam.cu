@@ -645,7 +645,7 @@ extern "C" int dec_kv_reorder(int n_layers, int n_kv_heads, int head_dim, int dt
   if (batch < 1 || batch > kReBatch || batch > kv_batch) return DEC_ERR_BATCH;
   if (max_ctx < 16 || max_ctx % 16) return DEC_ERR_ARG;
   if (!is_aligned(values, 16) || (fp8 && !is_aligned(scales, 4)) || !is_aligned(parents, 4) ||
-      !is_aligned(rows, 4))
+      !is_aligned(rows, 4) || !is_aligned(status, 4))
     return DEC_ERR_ALIGN;
   ReorderArgs a{};
   a.kv = static_cast<uint8_t*>(values);

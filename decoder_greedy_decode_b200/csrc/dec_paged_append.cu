@@ -554,7 +554,7 @@ extern "C" int dec_rope_apply(int n_tokens, int n_heads, int head_dim, int dtype
   if (rc != DEC_OK) return rc;
   if (n_tokens == 0) return DEC_OK;
   if (!x || !out || !positions) return DEC_ERR_NULL;
-  if (!is_aligned(x, 16) || !is_aligned(out, 16)) return DEC_ERR_ALIGN;
+  if (!is_aligned(x, 16) || !is_aligned(out, 16) || !is_aligned(positions, 4)) return DEC_ERR_ALIGN;
   if ((rc = check_stride(x_stride, n_tokens, n_heads, head_dim)) != DEC_OK) return rc;
   if ((rc = check_stride(out_stride, n_tokens, n_heads, head_dim)) != DEC_OK) return rc;
   if (x == out && n_tokens > 1 && x_stride != out_stride) return DEC_ERR_ARG;
@@ -599,7 +599,9 @@ extern "C" int dec_paged_append(const dec_pages* pool, const dec_page_map* map, 
   if (!io->k || !io->v || !io->positions) return DEC_ERR_NULL;
   if (io->n_q_heads ? (!io->q || !io->q_out) : (io->q || io->q_out)) return DEC_ERR_NULL;
   if (!(io->eps >= 0.f)) return DEC_ERR_ARG;
-  if (!is_aligned(io->k, 16) || !is_aligned(io->v, 16)) return DEC_ERR_ALIGN;
+  if (!is_aligned(io->k, 16) || !is_aligned(io->v, 16) || !is_aligned(io->positions, 4) ||
+      !is_aligned(io->seqs, 4) || !is_aligned(status, 4))
+    return DEC_ERR_ALIGN;
   if (io->n_q_heads && (!is_aligned(io->q, 16) || !is_aligned(io->q_out, 16)))
     return DEC_ERR_ALIGN;
   if ((io->q_norm && !is_aligned(io->q_norm, 16)) || (io->k_norm && !is_aligned(io->k_norm, 16)))

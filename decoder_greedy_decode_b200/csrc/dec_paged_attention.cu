@@ -1045,12 +1045,14 @@ extern "C" int dec_paged_attention(const dec_pages* pool, const dec_page_map* ma
       n_q_heads / pool->n_kv_heads > kMaxHeads)
     return DEC_ERR_SHAPE;
   if (batch > 1 && q_stride < static_cast<long long>(n_q_heads) * D) return DEC_ERR_SHAPE;
-  if (!is_aligned(q, 16) || (batch > 1 && q_stride % 8) || !is_aligned(workspace, 256) || !is_aligned(out, 8))
+  if (!is_aligned(q, 16) || (batch > 1 && q_stride % 8) || !is_aligned(workspace, 256) ||
+      !is_aligned(out, 8) || !is_aligned(lse, 4) || !is_aligned(rows, 4) || !is_aligned(status, 4))
     return DEC_ERR_ALIGN;
   if (workspace_bytes < dec_paged_attention_workspace_bytes(pool, batch, n_q_heads))
     return DEC_ERR_KV_SIZE;
   const int sms = device_sms();
   if (sms < 0) return sms;
+  if (paged_grid(pool, sms) * kWarps < pool->n_kv_heads) return DEC_ERR_DEVICE;   // (a warp per head)
   PagedArgs a{};
   a.pool = layer_view(pool, layer);
   a.table = map->table;

@@ -414,19 +414,19 @@ extern "C" size_t dec_pages_workspace_bytes(const dec_pages* pool, const dec_pag
 }
 
 static int check_pages_call(const dec_pages* pool, const dec_page_map* map, const void* in,
-                            const void* ws, size_t ws_bytes) {
+                            const void* ws, size_t ws_bytes, const int* status) {
   int rc = check_pool(pool);
   if (rc != DEC_OK) return rc;
   if ((rc = check_map(pool, map)) != DEC_OK) return rc;
   if (!in || !ws) return DEC_ERR_NULL;
-  if (!is_aligned(in, 4) || !is_aligned(ws, 256)) return DEC_ERR_ALIGN;
+  if (!is_aligned(in, 4) || !is_aligned(ws, 256) || !is_aligned(status, 4)) return DEC_ERR_ALIGN;
   return ws_bytes < layout_of(pool, map).total ? DEC_ERR_KV_SIZE : DEC_OK;
 }
 
 extern "C" int dec_pages_resize(const dec_pages* pool, const dec_page_map* map,
                                 const int32_t* new_rows, void* workspace, size_t workspace_bytes,
                                 int* status, void* stream) {
-  const int rc = check_pages_call(pool, map, new_rows, workspace, workspace_bytes);
+  const int rc = check_pages_call(pool, map, new_rows, workspace, workspace_bytes, status);
   if (rc != DEC_OK) return rc;
   const int sms = device_sms();
   if (sms < 0) return sms;
@@ -442,7 +442,7 @@ extern "C" int dec_pages_resize(const dec_pages* pool, const dec_page_map* map,
 extern "C" int dec_pages_compact(const dec_pages* pool, const dec_page_map* map, int32_t* n_live,
                                  void* workspace, size_t workspace_bytes, int* status,
                                  void* stream) {
-  const int rc = check_pages_call(pool, map, n_live, workspace, workspace_bytes);
+  const int rc = check_pages_call(pool, map, n_live, workspace, workspace_bytes, status);
   if (rc != DEC_OK) return rc;
   const int sms = device_sms();
   if (sms < 0) return sms;
@@ -461,7 +461,7 @@ extern "C" int dec_pages_fork(const dec_pages* pool, const dec_page_map* map,
   if (rc != DEC_OK) return rc;
   if ((rc = check_map(pool, map)) != DEC_OK) return rc;
   if (!parents) return DEC_ERR_NULL;
-  if (!is_aligned(parents, 4)) return DEC_ERR_ALIGN;
+  if (!is_aligned(parents, 4) || !is_aligned(status, 4)) return DEC_ERR_ALIGN;
   MapArgs a = map_args(pool, map, nullptr, status);
   a.in = parents;
   int cols = kForkCells / a.S;

@@ -281,6 +281,42 @@ def test_beam_search_equals_decoding_every_hypothesis(batch, eos):
     dec.close(), one.close()
 
 
+def test_beam_search_on_an_e4m3_cache():
+    """Every beam's cache and score agree with feeding its tokens one by one."""
+    s = synth.TINY
+    w = synth.model_weights(s, seed=13)
+    dec = Decoder(s, to_device(w), 8)
+    codes, scales = synth.kv_prefill(s, 8, 64, [25, 0, 0, 0, 40, 0, 0, 0], seed=8, kind="fp8")
+    tok, pos = synth.tokens(s.vocab, 2, seed=9).cuda(), torch.tensor([25, 40], dtype=torch.int32).cuda()
+    kv = dec.kv_cache(8, 64, "fp8")
+    kv.codes.copy_(codes.cuda()), kv.scales.copy_(scales.cuda())
+    n = 5
+    seqs, scores = dec.beam_search(kv, tok, pos, n, 4)
+    assert dec.check() == 0
+    one = dec.kv_cache(8, 64, "fp8")
+    for a in (one.codes, one.scales):
+        src = codes if a is one.codes else scales
+        for b in range(8):
+            a[:, :, b].copy_(src[:, :, b // 4 * 4].cuda())
+    total = torch.zeros(8, dtype=torch.float64)
+    ids, logits = torch.zeros(8, dtype=torch.int32, device="cuda"), torch.zeros((8, s.vocab), device="cuda")
+    feed, at = tok.repeat_interleave(4), pos.repeat_interleave(4)
+    for t in range(n):
+        dec.step(one, feed, at, ids, logits)
+        feed = seqs.view(8, n)[:, t].contiguous()
+        lp = torch.log_softmax(logits.double(), 1).cpu()
+        total += lp.gather(1, feed.cpu().long()[:, None])[:, 0]
+        at = at + 1
+    # (the same kernels on the same rows: the logits are equal, a score is a
+    # sum of n fp32 values of at most 64 off by 2^-19 + 2^-24 64 each)
+    assert bool(((scores.view(8).cpu().double() - total).abs() <= n * (LSE + 2.0 ** -18)).all())
+    for b in range(8):
+        m = int(pos[b // 4]) + n
+        assert torch.equal(kv.codes[:, :, b, :, :m], one.codes[:, :, b, :, :m])
+        assert torch.equal(kv.scales[:, :, b, :, :m], one.scales[:, :, b, :, :m])
+    dec.close()
+
+
 def test_beam_search_of_one_beam_is_greedy():
     s = synth.TINY
     w = synth.model_weights(s, seed=9)

@@ -335,3 +335,38 @@ def test_side_stream():
     got = c.attend(0, q, stream=s)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_windows_longer_than_the_context_and_of_one_row():
+    lens = [100, 31, 64, 1]
+    c = build(lens, 2, 64, 16, "fp8", seed=31)
+    q = torch.randn((4, 6, 64), generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    whole = attend(c, q, lens)
+    for w in (100, 1 << 30):
+        got = attend(c, q, lens, window=w)
+        assert torch.equal(got[0], whole[0]) and torch.equal(got[1], whole[1])
+    out, lse = attend(c, q, lens, window=1)
+    check(c, 0, q, lens, out, lse, 1)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_many_kv_heads_and_long_skewed_batches(fmt):
+    """More heads than a worker's CTA holds, and one sequence that all workers
+    share beside short ones."""
+    c = build([77, 5], 96, 64, 8, fmt, seed=32)
+    q = torch.randn((2, 96, 64), generator=torch.Generator().manual_seed(5)).bfloat16().cuda()
+    out, lse = attend(c, q, [77, 5])
+    check(c, 0, q, [77, 5], out, lse)
+    lens = [30000] + [3] * 9 + [0]
+    c = build(lens, 1, 128, 64, fmt, seed=33)
+    q = torch.randn((11, 8, 128), generator=torch.Generator().manual_seed(6)).bfloat16().cuda()
+    out, lse = attend(c, q, lens)
+    check(c, 0, q, lens, out, lse)
+
+
+def test_a_small_sequence_in_a_large_table():
+    """The table's width says nothing about the work: lengths do."""
+    c = build([50, 20], 2, 64, 16, "bf16", seed=34, max_rows=1 << 20)
+    q = torch.randn((2, 4, 64), generator=torch.Generator().manual_seed(7)).bfloat16().cuda()
+    out, lse = attend(c, q, [50, 20])
+    check(c, 0, q, [50, 20], out, lse)

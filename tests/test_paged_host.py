@@ -81,7 +81,9 @@ def test_page_calls_refuse_bad_arguments():
         assert f(a, b, P + 1, P, need, None, None) == -6
         assert f(a, b, P, P, need - 1, None, None) == -4
     assert L.dec_pages_fork(a, b, None, None, None) == -1
-    assert L.dec_pages_fork(a, b, P + 2, None, None) == -6
+    assert L.dec_pages_fork(a, b, P + 2, None, None) == -6 and L.dec_pages_fork(a, b, P, P + 2, None) == -6
+    assert L.dec_pages_resize(a, b, P, P, need, P + 1, None) == -6
+    assert L.dec_pages_compact(a, b, P, P, need, P + 1, None) == -6
 
 
 def test_attention_refuses_bad_arguments():
@@ -100,6 +102,8 @@ def test_attention_refuses_bad_arguments():
     assert go(stride=2040) == -2 and go(stride=2052) == -6
     assert go(q=P + 8) == -6 and go(ws=P + 16) == -6 and go(out=P + 4) == -6
     assert go(nb=need - 1) == -4
+    for rows, lse, status in ((P + 2, None, None), (P, P + 2, None), (P, None, P + 1)):
+        assert L.dec_paged_attention(a, b, 0, 4, 16, P, 2048, rows, 0, P, lse, P, need, status, None) == -6
 
 
 def test_append_refuses_bad_arguments():
@@ -123,6 +127,8 @@ def test_append_refuses_bad_arguments():
                        (capi.dec_rope(P, 130, 0, 1.0), -2), (capi.dec_rope(P, 7, 0, 1.0), -2),
                        (capi.dec_rope(P + 4, 64, 0, 1.0), -6)):
         assert go(rope=ctypes.pointer(rope)) == code
+    assert go(positions=P + 2) == -6 and go(seqs=P + 1) == -6
+    assert L.dec_paged_append(a, b, 0, ctypes.byref(append_io()), P + 2, None) == -6
     assert go(n_tokens=0) == 0      # nothing to do
 
 
@@ -137,6 +143,7 @@ def test_rotation_refuses_bad_arguments():
     assert go(D=96) == -2 and go(H=0) == -2 and go(rope=capi.dec_rope(P, 66, 0, 1.0)) == -2
     assert go(x=None) == -1 and go(out=None) == -1 and go(pos=None) == -1
     assert go(x=P + 4) == -6 and go(dt=1, x=P + 8) == -6 and go(xs=132) == -6 and go(os=64) == -2
+    assert go(pos=P + 2) == -6
     assert go(out=P, os=256) == -9   # in place with another stride
     assert go(n=0, x=None) == 0
 
@@ -169,6 +176,7 @@ def test_beam_calls_refuse_bad_arguments():
     assert re(val=None) == -1 and re(par=None) == -1 and re(rows=None) == -1 and re(dt=1) == -1
     assert re(D=32) == -2 and re(L_=0) == -2 and re(H=0) == -2 and re(dt=2) == -5
     assert re(b=0) == -3 and re(b=5) == -3 and re(b=65, kvb=100) == -3
+    assert L.dec_kv_reorder(2, 2, 64, 0, 4, 64, P, None, 4, P, P, P + 2, None) == -6
     assert re(ctx=24) == -9 and re(ctx=0) == -9 and re(val=P + 8) == -6 and re(par=P + 1) == -6
     assert L.dec_beam_backtrace(-1, 1, 1, P, P, P, None) == -9
     assert L.dec_beam_backtrace(1, 0, 1, P, P, P, None) == -9
