@@ -452,9 +452,14 @@ __global__ void __launch_bounds__(kMaxBeams * 32) groups_kernel(const BeamArgs a
 // ------------------------------------------------------- cache reordering
 // A CTA takes the same few rows of one (layer, K or V, head) of every moved
 // sequence: it copies the parents' rows to shared memory, waits, and writes
-// them, so the cache changes in place although parents are themselves moved.
+// them, so the cache changes in place although parents are themselves moved;
+// the next plane loads while one is stored.  Bound by HBM (a parent of several
+// is read once: its copies hit L2): 64 sequences of 200-420 rows of 28 layers,
+// 48 of them moved, 524 us = 5.4 TB/s of DRAM traffic; one plane at a time
+// 545, with 1 KB of a sequence 553; through bulk copies 728.
 constexpr int kReThreads = 256;
-constexpr int kRePiece = 1024;   // bytes of a sequence in one CTA
+constexpr int kRePiece = 512;    // bytes of a sequence in one CTA
+constexpr int kRePlanes = 8;     // planes that a CTA takes in turn
 constexpr int kReBatch = 64;
 
 struct ReorderArgs {
@@ -469,6 +474,7 @@ struct ReorderArgs {
 __global__ void __launch_bounds__(kReThreads) reorder_kernel(const ReorderArgs a) {
   extern __shared__ __align__(16) uint8_t s_data[];   // [moved][kRePiece], then scales
   __shared__ int s_to[kReBatch], s_from[kReBatch], s_rows[kReBatch];
+  __shared__ long long s_row[2][2][kReBatch];   // [buffer][from, to]
   __shared__ int s_n;
   const int tid = threadIdx.x;
   const int r0 = blockIdx.x * a.n_rows;
@@ -498,32 +504,52 @@ __global__ void __launch_bounds__(kReThreads) reorder_kernel(const ReorderArgs a
   }
   const int n = s_n;
   if (n == 0) return;
-  const int pieces = kRePiece / 16;
-  float* s_scale = reinterpret_cast<float*>(s_data + n * kRePiece);
-  for (long long plane = blockIdx.y; plane < a.planes; plane += gridDim.y) {
-    const long long lk = plane / a.H, h = plane % a.H;   // (layer, K or V), head
-    auto row_of = [&](int b) { return ((lk * a.kv_batch + b) * a.H + h) * a.max_ctx + r0; };
-    for (int i = tid; i < n * pieces; i += kReThreads) {
-      const int j = i / pieces, o = (i % pieces) * 16;
-      if (o < s_rows[j] * a.row_bytes)
-        cp_async16_cg(s_data + j * kRePiece + o, a.kv + row_of(s_from[j]) * a.row_bytes + o);
+  constexpr int pieces = kRePiece / 16;
+  const int room = n * kRePiece;   // bytes of one buffer
+  float* s_scale = reinterpret_cast<float*>(s_data + 2 * room);
+  auto load = [&](long long plane, int buf) {
+    // where each moved sequence reads and writes, once for all its pieces
+    if (tid < n) {
+      const long long lk = plane / a.H, h = plane % a.H;   // (layer, K or V), head
+      auto row_of = [&](int b) { return ((lk * a.kv_batch + b) * a.H + h) * a.max_ctx + r0; };
+      s_row[buf][0][tid] = row_of(s_from[tid]);
+      s_row[buf][1][tid] = row_of(s_to[tid]);
     }
-    if (a.scales)
-      for (int i = tid; i < n * a.n_rows; i += kReThreads)
-        if (i % a.n_rows < s_rows[i / a.n_rows])
-          s_scale[i] = a.scales[row_of(s_from[i / a.n_rows]) + i % a.n_rows];
-    cp_async_wait_all();
     __syncthreads();
     for (int i = tid; i < n * pieces; i += kReThreads) {
       const int j = i / pieces, o = (i % pieces) * 16;
       if (o < s_rows[j] * a.row_bytes)
-        *reinterpret_cast<uint4*>(a.kv + row_of(s_to[j]) * a.row_bytes + o) =
-            *reinterpret_cast<const uint4*>(s_data + j * kRePiece + o);
+        cp_async16_cg(s_data + buf * room + i * 16, a.kv + s_row[buf][0][j] * a.row_bytes + o);
     }
     if (a.scales)
-      for (int i = tid; i < n * a.n_rows; i += kReThreads)
-        if (i % a.n_rows < s_rows[i / a.n_rows])
-          a.scales[row_of(s_to[i / a.n_rows]) + i % a.n_rows] = s_scale[i];
+      for (int i = tid; i < n * a.n_rows; i += kReThreads) {
+        const int j = i / a.n_rows, r = i % a.n_rows;
+        if (r < s_rows[j])
+          cp_async4(s_scale + buf * n * a.n_rows + i, a.scales + s_row[buf][0][j] + r);
+      }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int buf = 0;
+  load(blockIdx.y, 0);
+  for (long long plane = blockIdx.y; plane < a.planes; plane += gridDim.y, buf ^= 1) {
+    if (plane + gridDim.y < a.planes) {   // the next plane loads while this one is stored
+      load(plane + gridDim.y, buf ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      cp_async_wait_all();
+    }
+    __syncthreads();
+    for (int i = tid; i < n * pieces; i += kReThreads) {
+      const int j = i / pieces, o = (i % pieces) * 16;
+      if (o < s_rows[j] * a.row_bytes)
+        *reinterpret_cast<uint4*>(a.kv + s_row[buf][1][j] * a.row_bytes + o) =
+            *reinterpret_cast<const uint4*>(s_data + buf * room + i * 16);
+    }
+    if (a.scales)
+      for (int i = tid; i < n * a.n_rows; i += kReThreads) {
+        const int j = i / a.n_rows, r = i % a.n_rows;
+        if (r < s_rows[j]) a.scales[s_row[buf][1][j] + r] = s_scale[buf * n * a.n_rows + i];
+      }
     __syncthreads();
   }
 }
@@ -660,12 +686,13 @@ extern "C" int dec_kv_reorder(int n_layers, int n_kv_heads, int head_dim, int dt
   a.parents = parents;
   a.rows = rows;
   a.status = status;
-  const int smem = batch * (kRePiece + (fp8 ? a.n_rows * 4 : 0));
+  const int smem = 2 * batch * (kRePiece + (fp8 ? a.n_rows * 4 : 0));
   static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem(reorder_kernel, kReBatch * (kRePiece + 64), allowed);
+  cudaError_t e = allow_smem(reorder_kernel, 2 * kReBatch * (kRePiece + 64), allowed);
   if (e != cudaSuccess) return cuda_failed(e);
   const unsigned x = static_cast<unsigned>((max_ctx + a.n_rows - 1) / a.n_rows);
-  const unsigned y = static_cast<unsigned>(a.planes < 65535 ? a.planes : 65535);
+  const long long per = (a.planes + kRePlanes - 1) / kRePlanes;
+  const unsigned y = static_cast<unsigned>(per < 65535 ? per : 65535);
   reorder_kernel<<<dim3(x, y), kReThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
   e = cudaGetLastError();
   return e == cudaSuccess ? DEC_OK : cuda_failed(e);
