@@ -395,24 +395,46 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
     if (turned && kind < 2) {
       // a passed pair is not multiplied (cosine 1 and sine 0 would turn an
       // infinity in it into NaN)
-#pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        if constexpr (M == kPairs) {
+      if constexpr (M == kPairs) {
+        auto turn = [&](int j) {
           const float2 u = pair(x, j);
-          const float2 y = fma2(make_float2(u.y, u.x), s2[j], mul2(u, c2[j]));
-          if (whole || pair_at<D, V>(false, j, o) < r) set(x, j, y);
+          return fma2(make_float2(u.y, u.x), s2[j], mul2(u, c2[j]));
+        };
+        if (whole) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) set(x, j, turn(j));
         } else {
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (pair_at<D, V>(false, j, o) < r) set(x, j, turn(j));
+        }
+      } else {
+        // pairs 2j, 2j + 1: both of one run, which turns or passes whole
+        // (kScalar: each for itself)
+        auto turn = [&](int j, bool first, bool second) {
           const float2 u = pair(x, j), v = pair(x, N / 2 + j);
           const float2 y = fma2(v, n2[j], mul2(u, c2[j]));
           const float2 z = fma2(u, s2[j], mul2(v, c2[j]));
-          if (whole || pair_at<D, V>(true, 2 * j, o) < r) {
+          if (first) {
             x[2 * j] = y.x;
             x[N + 2 * j] = z.x;
           }
-          if (whole || pair_at<D, V>(true, 2 * j + 1, o) < r) {
+          if (second) {
             x[2 * j + 1] = y.y;
             x[N + 2 * j + 1] = z.y;
           }
+        };
+        if constexpr (M == kHalf) {
+#pragma unroll
+          for (int k = 0; k < K / 2; ++k)
+            if ((8 * k + o) * V < r) {
+#pragma unroll
+              for (int j = k * V / 2; j < (k + 1) * V / 2; ++j) turn(j, true, true);
+            }
+        } else {
+#pragma unroll
+          for (int j = 0; j < NC; ++j)
+            turn(j, pair_at<D, V>(true, 2 * j, o) < r, pair_at<D, V>(true, 2 * j + 1, o) < r);
         }
       }
     }
