@@ -822,9 +822,28 @@ __device__ __forceinline__ const float* state_of(const PagedArgs& a, const Item&
   const int words = a.rep * (D + 2);
   return a.part + (static_cast<long long>(it.d.x + i) * a.Hkv + it.g) * (2 * words) + (i == 0 ? words : 0);
 }
+// The sums of states first, first + step, ... of this lane's elements, loaded
+// beside the weights instead of after them.
+constexpr int kPre = 8;
+template <int D>
+__device__ __forceinline__ void preload(const PagedArgs& a, const Item& it, int first, int step,
+                                        float (&v)[kPre][D / 32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < kPre; ++k) {
+    const int i = first + k * step;
+    if (i < it.d.y) {
+      const float* p = state_of(a, it, D, i) + it.hh * D + lane;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) v[k][e] = __ldcg(p + 32 * e);
+    }
+  }
+}
 template <int D>
 __device__ __forceinline__ void join_by_warp(const PagedArgs& a, const Item& it) {
   const int lane = threadIdx.x & 31, n = it.d.y;
+  float v[kPre][D / 32];
+  preload<D>(a, it, 0, 1, v);
   float m = -INFINITY, l = 0.f;
   if (lane < n) {
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(state_of(a, it, D, lane) + a.rep * D) + it.hh);
@@ -838,30 +857,39 @@ __device__ __forceinline__ void join_by_warp(const PagedArgs& a, const Item& it)
   float acc[D / 32];
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPre; ++i) {
+    const float wi = __shfl_sync(0xffffffffu, w, i);   // (0 behind the last state)
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc[e] = i < n ? fmaf(v[i][e], wi, acc[e]) : acc[e];
+  }
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* v = state_of(a, it, D, i) + it.hh * D + lane;
+  for (int i = kPre; i < n; ++i) {
+    const float* p = state_of(a, it, D, i) + it.hh * D + lane;
     const float wi = __shfl_sync(0xffffffffu, w, i);
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(__ldcg(v + 32 * e), wi, acc[e]);
+    for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(__ldcg(p + 32 * e), wi, acc[e]);
   }
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) it.out[e * 32 + lane] = acc[e] / l;
   if (lane == 0 && it.lse) *it.lse = (M + log2f(l)) * 0.6931471805599453f;
 }
-// s_w: a float per worker; every thread of the CTA.
+// s_w: two floats per worker; every thread of the CTA.
 template <int D>
 __device__ __forceinline__ void join_by_cta(const PagedArgs& a, const Item& it, float* s_w) {
   __shared__ float s_acc[kWarps][D];
   __shared__ float s_red[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = it.d.y;
+  float v[kPre][D / 32];
+  preload<D>(a, it, warp, kWarps, v);
   float m = -INFINITY;
   bool poison = false;
+  float2* s_ml = reinterpret_cast<float2*>(s_w);
   for (int i = tid; i < n; i += kThreads) {
-    const float v = __ldcg(state_of(a, it, D, i) + a.rep * D + 2 * it.hh);
-    s_w[i] = v;
-    poison |= v != v;
-    m = fmaxf(m, v);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(state_of(a, it, D, i) + a.rep * D) + it.hh);
+    s_ml[i] = ml;
+    poison |= ml.x != ml.x;
+    m = fmaxf(m, ml.x);
   }
   m = warp_max(m);
   if (lane == 0) s_red[warp] = m;
@@ -869,10 +897,11 @@ __device__ __forceinline__ void join_by_cta(const PagedArgs& a, const Item& it, 
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_red[w]);
   float l = 0.f;
-  for (int i = tid; i < n; i += kThreads) {
-    const float w = s_w[i] == -INFINITY ? 0.f : ex2(s_w[i] - m);
-    l += __ldcg(state_of(a, it, D, i) + a.rep * D + 2 * it.hh + 1) * w;
-    s_w[i] = w;
+  for (int i = tid; i < n; i += kThreads) {   // (the weight takes the place of m)
+    const float2 ml = s_ml[i];
+    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+    l += ml.y * w;
+    s_ml[i].x = w;
   }
   l = warp_sum(l);
   __syncthreads();   // s_red has been read, s_w is complete
@@ -880,12 +909,20 @@ __device__ __forceinline__ void join_by_cta(const PagedArgs& a, const Item& it, 
   float acc[D / 32];
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < n; i += kWarps) {
-    const float* v = state_of(a, it, D, i) + it.hh * D + lane;
-    const float w = s_w[i];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(__ldcg(v + 32 * e), w, acc[e]);
+  for (int k = 0; k < kPre; ++k) {
+    const int i = warp + k * kWarps;
+    if (i < n) {
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(v[k][e], s_ml[i].x, acc[e]);
+    }
+  }
+#pragma unroll 4
+  for (int i = warp + kPre * kWarps; i < n; i += kWarps) {
+    const float* p = state_of(a, it, D, i) + it.hh * D + lane;
+    const float w = s_ml[i].x;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(__ldcg(p + 32 * e), w, acc[e]);
   }
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) s_acc[warp][e * 32 + lane] = acc[e];
