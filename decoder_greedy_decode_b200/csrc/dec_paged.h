@@ -52,7 +52,8 @@ inline int check_pool(const dec_pages* p) {
 inline int check_map(const dec_pages* p, const dec_page_map* m) {
   if (!m || !m->table || !m->rows || !m->refs) return DEC_ERR_NULL;
   if (m->n_seqs < 1 || m->n_seqs > 4096) return DEC_ERR_BATCH;
-  if (m->width < 1 || static_cast<long long>(m->width) * p->page_rows > (1ll << 30))
+  if (m->width < 1 || static_cast<long long>(m->width) * p->page_rows > (1ll << 30) ||
+      static_cast<long long>(m->n_seqs) * m->width > INT32_MAX)
     return DEC_ERR_SHAPE;
   if (!is_aligned(m->table, 4) || !is_aligned(m->rows, 4) || !is_aligned(m->refs, 4))
     return DEC_ERR_ALIGN;

@@ -548,7 +548,8 @@ typedef struct dec_page_map {
   int32_t *rows;    /* [n_seqs] rows that each sequence holds */
   int32_t *refs;    /* [n_pages] */
   int n_seqs;       /* 1..4096 */
-  int width;        /* pages per sequence; width * page_rows <= 2^30 */
+  int width;        /* pages per sequence; width * page_rows <= 2^30 and
+                     * n_seqs * width < 2^31 */
 } dec_page_map;
 
 /* Device scratch (256-byte aligned, uninitialised) of dec_pages_resize and
@@ -577,8 +578,9 @@ int dec_pages_resize(const dec_pages *pool, const dec_page_map *map, const int32
 /* All sequences at once become copies of their parents: sequence s holds the
  * pages and rows that parents[s] (int32 [n_seqs], device) held before the
  * call; a negative parent empties it.  No data moves: pages are shared, and
- * dec_pages_resize copies a shared page before it is written.  Pages that no
- * sequence holds any more are free.  A parent >= n_seqs raises
+ * dec_pages_resize copies a shared page before it grows into it (rows that are
+ * reserved but not yet written are shared as well: crop to the written ones
+ * before a fork).  Pages that no sequence holds any more are free.  A parent >= n_seqs raises
  * DEC_DEV_BAD_PAGE and nothing is changed; a table entry outside
  * [-1, n_pages) raises it and counts as -1.  Asynchronous on `stream`. */
 int dec_pages_fork(const dec_pages *pool, const dec_page_map *map, const int32_t *parents,

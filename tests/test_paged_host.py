@@ -67,6 +67,13 @@ def test_maps_that_every_call_refuses(kw, code):
     assert capi.dec_pages_workspace_bytes(pool(), pmap(**kw)) == 0
 
 
+def test_a_table_of_more_than_int32_cells_is_refused():
+    big = pmap(n_seqs=4096, width=1 << 19)    # 2^31 cells
+    assert calls(pool(), big) == [-2] * 5
+    assert capi.dec_pages_workspace_bytes(pool(), big) == 0
+    assert capi.dec_pages_workspace_bytes(pool(), pmap(n_seqs=4095, width=1 << 19)) > 0
+
+
 def test_page_calls_refuse_bad_arguments():
     L = capi.lib()
     a, b = ctypes.byref(pool()), ctypes.byref(pmap())
