@@ -59,9 +59,6 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxHeads = 8;  // query heads per KV head (the N of the MMA)
 
-#ifndef KCF
-#define KCF(D, FP8) ((FP8) ? 3 : (D) == 128 ? 2 : 3)
-#endif
 struct PagedArgs {
   PoolView pool;
   const int32_t* table;
@@ -175,7 +172,10 @@ struct Cfg {
   static constexpr int TR = 16 * NS;                       // rows of a tile
   static constexpr int HB = TR * D * ES;                   // bytes of its K (or V) rows
   static constexpr int SB = FP8 ? 2 * TR * 4 : 0;          // bytes of its scales
-  static constexpr int CTAS = KCF(D, FP8);                 // CTAs of an SM
+  // CTAs of an SM.  E4M3 is bound by what its warps issue: 3 (64 sequences of
+  // 2K to 4K rows: 95 us, 118 with 2).  bf16 heads of 128 want the registers of
+  // 2 (32 sequences of 16K to 32K rows: 458 us, 496 with 3)
+  static constexpr int CTAS = !FP8 && D == 128 ? 2 : 3;
   static constexpr int ROOM = (227 * 1024 / CTAS - 3072) / kWarps;   // a warp's share
   static constexpr int S = ROOM / (2 * HB + SB) < 8 ? ROOM / (2 * HB + SB) : 8;  // ring slots
   static constexpr int SMEM = 1024 + kWarps * S * (2 * HB + SB);
