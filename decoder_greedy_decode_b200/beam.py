@@ -23,6 +23,14 @@ class Selection(NamedTuple):
     done: Optional[torch.Tensor]   # uint8 [groups, k]; None without an end token
 
 
+def _result(t, name: str, dtype, shape, like: torch.Tensor) -> torch.Tensor:
+    """`t` if it is given and fits, else a new tensor on `like`'s device."""
+    if t is None:
+        return like.new_empty(shape, dtype=dtype)
+    tensors.check_tensor(t, name, dtype, shape, like.device)
+    return t
+
+
 def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = None,
                 done: Optional[torch.Tensor] = None, eos: int = -1,
                 out_scores: Optional[torch.Tensor] = None,
@@ -60,20 +68,14 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = N
     shape = (G, max(k, 0))
     if out_scores is None and out_parents is None and out_tokens is None:
         # (one allocation for the three)
-        bits, out_parents, out_tokens = torch.empty((3,) + shape, dtype=torch.int32, device=dev).unbind()
+        bits, out_parents, out_tokens = scores.new_empty((3,) + shape, dtype=torch.int32).unbind()
         out_scores = bits.view(torch.float32)
-
-    def result(t, name, dtype):
-        if t is None:
-            return torch.empty(shape, dtype=dtype, device=dev)
-        tensors.check_tensor(t, name, dtype, shape, dev)
-        return t
-
-    out_scores = result(out_scores, "out_scores", torch.float32)
-    out_parents = result(out_parents, "out_parents", torch.int32)
-    out_tokens = result(out_tokens, "out_tokens", torch.int32)
+    else:
+        out_scores = _result(out_scores, "out_scores", torch.float32, shape, scores)
+        out_parents = _result(out_parents, "out_parents", torch.int32, shape, scores)
+        out_tokens = _result(out_tokens, "out_tokens", torch.int32, shape, scores)
     if out_done is not None or eos >= 0:
-        out_done = result(out_done, "out_done", torch.uint8)
+        out_done = _result(out_done, "out_done", torch.uint8, shape, scores)
     rc = capi.lib().dec_beam_select(
         G, W, V, k, tensors.dtype_code(logits, "logits"), logits.data_ptr(), row, scores.data_ptr(),
         None if done is None else done.data_ptr(), eos, out_scores.data_ptr(),

@@ -225,14 +225,14 @@ class PagedKV:
         if rows is not None:
             tensors.check_tensor(rows, "rows", torch.int32, (B,), dev)
         if out is None:
-            out = torch.empty(shape, dtype=torch.float32, device=dev)
+            out = q.new_empty(shape, dtype=torch.float32)
         else:
             tensors.check_tensor(out, "out", torch.float32, shape, dev)
         nb = self._attend_bytes.get((B, Hq))
         if nb is None:
             nb = capi.dec_paged_attention_workspace_bytes(self.pool, B, Hq)
             self._attend_bytes[(B, Hq)] = nb
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev) if return_lse else None
+        lse = q.new_empty((B, Hq), dtype=torch.float32) if return_lse else None
         ws = torch.empty(nb or 256, dtype=torch.uint8, device=dev)
         rc = capi.lib().dec_paged_attention(
             *self._refs, layer, B, Hq, q.data_ptr(), q.stride(0),
