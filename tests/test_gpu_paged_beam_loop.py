@@ -95,3 +95,73 @@ def test_beam_search_over_pages(fmt, D, P, window):
     assert torch.equal(torch.bincount(held[held >= 0].long(), minlength=c.n_pages).int(), c.refs.cpu())
     c.resize(rows_now(0))
     assert int(c.refs.sum()) == 0 and int((c.table >= 0).sum()) == 0
+
+
+def search_state(fmt):
+    """A cache of two groups of two beams with 21 shared rows (a page and a
+    part of the next), and the buffers of a step."""
+    g = torch.Generator().manual_seed(5)
+    G, W, H, Hq, D, P, V = 2, 2, 2, 4, 64, 16, 300
+    S = G * W
+    c = PagedKV.create(1, 24, P, H, D, S, 64, dtype=fmt)
+    c.resize(torch.tensor([21, 0, 21, 0], dtype=torch.int32).cuda())
+    seq = torch.tensor([0] * 21 + [2] * 21, dtype=torch.int32).cuda()
+    pos = torch.arange(21, dtype=torch.int32).repeat(2).cuda()
+    k, v = (torch.randn((42, H, D), generator=g).bfloat16().cuda() for _ in range(2))
+    c.append(0, k, v, pos, seqs=seq)
+    c.fork(torch.tensor([0, 0, 2, 2], dtype=torch.int32).cuda())
+    steps = [dict(logits=torch.randn((G, W, V), generator=g).cuda(),
+                  k=torch.randn((S, H, D), generator=g).bfloat16().cuda(),
+                  v=torch.randn((S, H, D), generator=g).bfloat16().cuda(),
+                  q=torch.randn((S, Hq, D), generator=g).bfloat16().cuda()) for _ in range(14)]
+    return c, Rope(D, theta=1e4), torch.tensor([[0.0, -1.0]] * G).cuda(), \
+        torch.tensor([0, 0, 2, 2], dtype=torch.int32).cuda(), \
+        torch.full((S,), 21, dtype=torch.int32).cuda(), steps
+
+
+def search_step(c, rope, scores, base, pos, x, stream=None):
+    r = beam.beam_select(x["logits"], scores, out_scores=scores, stream=stream)
+    with torch.cuda.stream(stream):
+        parents = r.parents.view(-1) + base
+        rows = pos + 1
+    c.fork(parents, stream=stream)
+    c.resize(rows, stream=stream)
+    q = c.append(0, x["k"], x["v"], pos, rope=rope, q=x["q"], stream=stream)
+    out = c.attend(0, q, stream=stream)
+    with torch.cuda.stream(stream):
+        pos.copy_(rows)
+    return r.tokens, out
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_the_same_search_on_a_side_stream_and_in_a_graph(fmt):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    c, *rest, steps = search_state(fmt)
+    want = [search_step(c, *rest, x) for x in steps]
+    assert c.check() == 0
+    end = c.table.clone()
+
+    c, *rest, _ = search_state(fmt)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [search_step(c, *rest, x, stream=side) for x in steps]
+    side.synchronize()
+    for (t, o), (t0, o0) in zip(got, want):
+        assert torch.equal(t, t0) and torch.equal(o, o0)
+    assert torch.equal(c.table, end) and c.check() == 0
+
+    c, *rest, _ = search_state(fmt)
+    now = {n: x.clone() for n, x in steps[0].items()}
+    t, o = search_step(c, *rest, now)   # (the first call sets up what a capture may not)
+    assert torch.equal(t, want[0][0]) and torch.equal(o, want[0][1])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        t, o = search_step(c, *rest, now)
+    for x, (t0, o0) in zip(steps[1:], want[1:]):
+        for n in now:
+            now[n].copy_(x[n])
+        graph.replay()
+        assert torch.equal(t, t0) and torch.equal(o, o0)
+    assert torch.equal(c.table, end) and c.check() == 0
