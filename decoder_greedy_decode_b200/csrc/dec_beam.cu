@@ -18,6 +18,11 @@
 // equal logits, or -inf for most of a masked vocabulary, or rising ones), the
 // chunk is read again with keys in place of logits: the bound of every batch
 // is then exact enough that at most 64 k keys of a batch are gathered.
+//
+// Measured: 16 groups of 4 rows of 151936 fp32 logits 17.6 us (14.8 the rows,
+// 39 MB), 26.9 with a 64-bit key for every logit; one group 8.8 us.  One wave of
+// CTAs: their load, bound and gather phases coincide.  Both launches in one
+// cooperative kernel took 23 us.
 #include <cuda_runtime.h>
 
 #include "dec.h"

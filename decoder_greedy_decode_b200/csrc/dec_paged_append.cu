@@ -14,9 +14,11 @@
 // memory; the sines and cosines of a token are computed once by the warp,
 // each lane a quarter of what its eight lanes need, and kept in registers
 // for all rows.  The next rows are loaded before the present ones are used.
-// The bound is HBM (every input read once, every output written once); with a
-// row per warp and IEEE divisions the issue slots were it (193 instructions a
-// row, 180 us for 16384 tokens with E4M3 pages; floor 36).
+// The floor is HBM (every input read once, every output written once): 8192 x 32
+// fp32 heads rotated alone take 44.6 us = 6.0 TB/s.  With norms and E4M3 pages
+// the issue slots are the bound (70 % used): 16384 tokens of 16 + 8 + 8 heads
+// 55.8 us for 36 us of bytes; with a row per warp and IEEE divisions 180 us
+// (193 instructions a row against 75).
 //
 // E4M3 codes are RNE(x / scale) of the IEEE quotient.  The quotient comes from
 // a correctly rounded reciprocal y of the scale by one residual step
@@ -295,200 +297,200 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
   }
 #pragma unroll 1
   for (int job = job0; job < jobs; job += hop) {
-  const int t = job / per_token, part = job % per_token;
-  const int pos = now.pos;
-  bool keep = !CACHE || pos >= 0;   // (rotation alone: the row of padding is copied)
-  long long row0 = 0;   // element of the token's row of head 0 in the pages
-  if (CACHE && keep) {
-    const int bad = now.bad | (!now.bad && (now.page < 0 || now.page >= a.pool.n_pages) ? DEC_DEV_BAD_PAGE : 0);
-    if (bad) {
-      if (a.status && lane == 0 && part == 0) atomicOr(a.status, bad);
-      keep = false;
+    const int t = job / per_token, part = job % per_token;
+    const int pos = now.pos;
+    bool keep = !CACHE || pos >= 0;   // (rotation alone: the row of padding is copied)
+    long long row0 = 0;   // element of the token's row of head 0 in the pages
+    if (CACHE && keep) {
+      const int bad = now.bad | (!now.bad && (now.page < 0 || now.page >= a.pool.n_pages) ? DEC_DEV_BAD_PAGE : 0);
+      if (bad) {
+        if (a.status && lane == 0 && part == 0) atomicOr(a.status, bad);
+        keep = false;
+      }
+      row0 = now.page * a.pool.page_stride + static_cast<long long>(pos & ((1 << a.pool.shift) - 1)) * D;
     }
-    row0 = now.page * a.pool.page_stride + static_cast<long long>(pos & ((1 << a.pool.shift) - 1)) * D;
-  }
-  now = then;
-  find(now);
-  then = look(job + 2 * hop);
-  const bool turned = a.phases && pos >= 0;
+    now = then;
+    find(now);
+    then = look(job + 2 * hop);
+    const bool turned = a.phases && pos >= 0;
 
-  // cosine and sine of the lane's pairs, packed as the rotation uses them:
-  // of two neighbouring pairs (half-split), or twice the same pair
-  constexpr int NC = M == kPairs ? N : N / 2;
-  float2 c2[NC], s2[NC], n2[NC];   // cosine, sine, -sine (neighbours: s2 = (-sine, sine))
-  if (turned) {
-    float c[N / 4], s[N / 4];
+    // cosine and sine of the lane's pairs, packed as the rotation uses them:
+    // of two neighbouring pairs (half-split), or twice the same pair
+    constexpr int NC = M == kPairs ? N : N / 2;
+    float2 c2[NC], s2[NC], n2[NC];   // cosine, sine, -sine (neighbours: s2 = (-sine, sine))
+    if (turned) {
+      float c[N / 4], s[N / 4];
 #pragma unroll
-    for (int j = 0; j < N / 4; ++j) {
-      // the angle in half turns, [-1, 1): the top 32 bits of the fraction
-      const uint64_t ph = phase[j] * static_cast<uint64_t>(pos);
-      sincospif(static_cast<float>(static_cast<int32_t>(ph >> 32)) * 0x1p-31f, &s[j], &c[j]);
-      c[j] *= a.mscale;
-      s[j] *= a.mscale;
-    }
-    float cs[N], sn[N];
+      for (int j = 0; j < N / 4; ++j) {
+        // the angle in half turns, [-1, 1): the top 32 bits of the fraction
+        const uint64_t ph = phase[j] * static_cast<uint64_t>(pos);
+        sincospif(static_cast<float>(static_cast<int32_t>(ph >> 32)) * 0x1p-31f, &s[j], &c[j]);
+        c[j] *= a.mscale;
+        s[j] *= a.mscale;
+      }
+      float cs[N], sn[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      cs[j] = __shfl_sync(0xffffffffu, c[j % (N / 4)], j / (N / 4) * 8 + o);
-      sn[j] = __shfl_sync(0xffffffffu, s[j % (N / 4)], j / (N / 4) * 8 + o);
-    }
+      for (int j = 0; j < N; ++j) {
+        cs[j] = __shfl_sync(0xffffffffu, c[j % (N / 4)], j / (N / 4) * 8 + o);
+        sn[j] = __shfl_sync(0xffffffffu, s[j % (N / 4)], j / (N / 4) * 8 + o);
+      }
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      if (M == kPairs) {
-        c2[j] = make_float2(cs[j], cs[j]);
-        s2[j] = make_float2(-sn[j], sn[j]);
-      } else {
-        c2[j] = make_float2(cs[2 * j], cs[2 * j + 1]);
-        s2[j] = make_float2(sn[2 * j], sn[2 * j + 1]);
-        n2[j] = make_float2(-sn[2 * j], -sn[2 * j + 1]);
+      for (int j = 0; j < NC; ++j) {
+        if (M == kPairs) {
+          c2[j] = make_float2(cs[j], cs[j]);
+          s2[j] = make_float2(-sn[j], sn[j]);
+        } else {
+          c2[j] = make_float2(cs[2 * j], cs[2 * j + 1]);
+          s2[j] = make_float2(sn[2 * j], sn[2 * j + 1]);
+          n2[j] = make_float2(-sn[2 * j], -sn[2 * j + 1]);
+        }
       }
     }
-  }
-  // element of a rotated row that x[i] is, one by one
-  auto element = [&](int i) {
-    const int p = pair_at<D, V>(true, i % N, o);
-    return i < N ? first_of<D>(p, a.rot) : second_of<D>(p, a.rot);
-  };
-  auto pair = [](const float* v, int i) { return make_float2(v[2 * i], v[2 * i + 1]); };
-  auto set = [](float* v, int i, float2 y) {
-    v[2 * i] = y.x;
-    v[2 * i + 1] = y.y;
-  };
-  const bool whole = 2 * r == D;   // every pair turns
+    // element of a rotated row that x[i] is, one by one
+    auto element = [&](int i) {
+      const int p = pair_at<D, V>(true, i % N, o);
+      return i < N ? first_of<D>(p, a.rot) : second_of<D>(p, a.rot);
+    };
+    auto pair = [](const float* v, int i) { return make_float2(v[2 * i], v[2 * i + 1]); };
+    auto set = [](float* v, int i, float2 y) {
+      v[2 * i] = y.x;
+      v[2 * i + 1] = y.y;
+    };
+    const bool whole = 2 * r == D;   // every pair turns
 
 #pragma unroll 1
-  for (int quad = part; quad < quads; quad += per_token) {
-    const int kind = kind_of(quad), head = head_of(quad, kind);
-    const bool live = keep && head < (kind == 0 ? a.Hq : a.Hkv);
-    const bool loose = M == kScalar && kind < 2 && a.phases;   // element by element
-    float x[2 * N];
-    if constexpr (M != kScalar) {
+    for (int quad = part; quad < quads; quad += per_token) {
+      const int kind = kind_of(quad), head = head_of(quad, kind);
+      const bool live = keep && head < (kind == 0 ? a.Hq : a.Hkv);
+      const bool loose = M == kScalar && kind < 2 && a.phases;   // element by element
+      float x[2 * N];
+      if constexpr (M != kScalar) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) raw[k].get(x + k * V);
-      fetch();
-    } else {
-      const T* p = source(t, kind, head);
-#pragma unroll
-      for (int i = 0; i < 2 * N; ++i) x[i] = ld1(p + (loose ? element(i) : plain_at[i / V] + i % V));
-    }
-    const uint16_t* gain = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
-    if (gain) {
-      float g[2 * N];
-      if (loose) {
-#pragma unroll
-        for (int i = 0; i < 2 * N; ++i) g[i] = ld1(gain + element(i));
+        for (int k = 0; k < K; ++k) raw[k].get(x + k * V);
+        fetch();
       } else {
+        const T* p = source(t, kind, head);
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          Raw<uint16_t, V> w;
-          w.load(gain + split_at[k]);
-          w.get(g + k * V);
-        }
+        for (int i = 0; i < 2 * N; ++i) x[i] = ld1(p + (loose ? element(i) : plain_at[i / V] + i % V));
       }
-      float2 ss = make_float2(0.f, 0.f);
+      const uint16_t* gain = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
+      if (gain) {
+        float g[2 * N];
+        if (loose) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) ss = fma2(pair(x, i), pair(x, i), ss);
-      const float f = rsqrtf(row_sum(ss.x + ss.y) * (1.0f / D) + a.eps);
-#pragma unroll
-      for (int i = 0; i < N; ++i) set(x, i, mul2(mul2(pair(x, i), make_float2(f, f)), pair(g, i)));
-    }
-    if (turned && kind < 2) {
-      // a passed pair is not multiplied (cosine 1 and sine 0 would turn an
-      // infinity in it into NaN)
-      if constexpr (M == kPairs) {
-        auto turn = [&](int j) {
-          const float2 u = pair(x, j);
-          return fma2(make_float2(u.y, u.x), s2[j], mul2(u, c2[j]));
-        };
-        if (whole) {
-#pragma unroll
-          for (int j = 0; j < N; ++j) set(x, j, turn(j));
+          for (int i = 0; i < 2 * N; ++i) g[i] = ld1(gain + element(i));
         } else {
 #pragma unroll
-          for (int j = 0; j < N; ++j)
-            if (pair_at<D, V>(false, j, o) < r) set(x, j, turn(j));
+          for (int k = 0; k < K; ++k) {
+            Raw<uint16_t, V> w;
+            w.load(gain + split_at[k]);
+            w.get(g + k * V);
+          }
         }
-      } else {
-        // pairs 2j, 2j + 1: both of one run, which turns or passes whole
-        // (kScalar: each for itself)
-        auto turn = [&](int j, bool first, bool second) {
-          const float2 u = pair(x, j), v = pair(x, N / 2 + j);
-          const float2 y = fma2(v, n2[j], mul2(u, c2[j]));
-          const float2 z = fma2(u, s2[j], mul2(v, c2[j]));
-          if (first) {
-            x[2 * j] = y.x;
-            x[N + 2 * j] = z.x;
-          }
-          if (second) {
-            x[2 * j + 1] = y.y;
-            x[N + 2 * j + 1] = z.y;
-          }
-        };
-        if constexpr (M == kHalf) {
+        float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int k = 0; k < K / 2; ++k)
-            if ((8 * k + o) * V < r) {
+        for (int i = 0; i < N; ++i) ss = fma2(pair(x, i), pair(x, i), ss);
+        const float f = rsqrtf(row_sum(ss.x + ss.y) * (1.0f / D) + a.eps);
 #pragma unroll
-              for (int j = k * V / 2; j < (k + 1) * V / 2; ++j) turn(j, true, true);
+        for (int i = 0; i < N; ++i) set(x, i, mul2(mul2(pair(x, i), make_float2(f, f)), pair(g, i)));
+      }
+      if (turned && kind < 2) {
+        // a passed pair is not multiplied (cosine 1 and sine 0 would turn an
+        // infinity in it into NaN)
+        if constexpr (M == kPairs) {
+          auto turn = [&](int j) {
+            const float2 u = pair(x, j);
+            return fma2(make_float2(u.y, u.x), s2[j], mul2(u, c2[j]));
+          };
+          if (whole) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) set(x, j, turn(j));
+          } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+              if (pair_at<D, V>(false, j, o) < r) set(x, j, turn(j));
+          }
+        } else {
+          // pairs 2j, 2j + 1: both of one run, which turns or passes whole
+          // (kScalar: each for itself)
+          auto turn = [&](int j, bool first, bool second) {
+            const float2 u = pair(x, j), v = pair(x, N / 2 + j);
+            const float2 y = fma2(v, n2[j], mul2(u, c2[j]));
+            const float2 z = fma2(u, s2[j], mul2(v, c2[j]));
+            if (first) {
+              x[2 * j] = y.x;
+              x[N + 2 * j] = z.x;
             }
+            if (second) {
+              x[2 * j + 1] = y.y;
+              x[N + 2 * j + 1] = z.y;
+            }
+          };
+          if constexpr (M == kHalf) {
+#pragma unroll
+            for (int k = 0; k < K / 2; ++k)
+              if ((8 * k + o) * V < r) {
+#pragma unroll
+                for (int j = k * V / 2; j < (k + 1) * V / 2; ++j) turn(j, true, true);
+              }
+          } else {
+#pragma unroll
+            for (int j = 0; j < NC; ++j)
+              turn(j, pair_at<D, V>(true, 2 * j, o) < r, pair_at<D, V>(true, 2 * j + 1, o) < r);
+          }
+        }
+      }
+      auto write = [&](auto* p) {
+        if (loose) {
+#pragma unroll
+          for (int i = 0; i < 2 * N; ++i) put1(p + element(i), x[i]);
         } else {
 #pragma unroll
-          for (int j = 0; j < NC; ++j)
-            turn(j, pair_at<D, V>(true, 2 * j, o) < r, pair_at<D, V>(true, 2 * j + 1, o) < r);
+          for (int k = 0; k < K; ++k) put<V>(p + (kind < 2 ? split_at[k] : plain_at[k]), x + k * V);
         }
+      };
+      if (kind == 0) {
+        if (live) write(static_cast<TO*>(a.q_out) + t * a.q_out_stride + head * D);
+        continue;
       }
-    }
-    auto write = [&](auto* p) {
-      if (loose) {
-#pragma unroll
-        for (int i = 0; i < 2 * N; ++i) put1(p + element(i), x[i]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < K; ++k) put<V>(p + (kind < 2 ? split_at[k] : plain_at[k]), x + k * V);
-      }
-    };
-    if (kind == 0) {
-      if (live) write(static_cast<TO*>(a.q_out) + t * a.q_out_stride + head * D);
-      continue;
-    }
-    if constexpr (CACHE > 0) {
-      const long long e = row0 + (static_cast<long long>(head) << a.pool.shift) * D;
-      if constexpr (CACHE == 1) {
-        if (live) write(reinterpret_cast<uint16_t*>(kind == 1 ? a.pool.k : a.pool.v) + e);
-      } else {
-        float am = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2 * N; ++i) am = fmaxf(am, fabsf(x[i]));
-        am = fmaxf(row_max(am), 1.17549435e-38f);  // 2^-126
-        float sc, den;   // the scale, and the scale times a power of two
-        if (am >= 0x1p-60f && am <= 0x1p100f) {
-          constexpr float y = 1.0f / 448.0f;
-          const float s0 = am * y;
-          den = sc = fmaf(fmaf(-s0, 448.0f, am), y, s0);
+      if constexpr (CACHE > 0) {
+        const long long e = row0 + (static_cast<long long>(head) << a.pool.shift) * D;
+        if constexpr (CACHE == 1) {
+          if (live) write(reinterpret_cast<uint16_t*>(kind == 1 ? a.pool.k : a.pool.v) + e);
         } else {
-          // far from 1: the row and its scale times a power of two, exact
-          // where a code is not 0 (an infinite scale: 0, or NaN for infinities)
-          sc = __fdiv_rn(am, 448.0f);
-          const float u = am < 1.f ? 0x1p100f : isinf(sc) ? 0.f : 0x1p-60f;
-          den = isinf(sc) ? 1.f : sc * u;
+          float am = 0.f;
 #pragma unroll
-          for (int i = 0; i < 2 * N; ++i) x[i] *= u;
-        }
-        const float inv = __frcp_rn(den);
-        const float2 inv2 = make_float2(inv, inv), neg2 = make_float2(-den, -den);
+          for (int i = 0; i < 2 * N; ++i) am = fmaxf(am, fabsf(x[i]));
+          am = fmaxf(row_max(am), 1.17549435e-38f);  // 2^-126
+          float sc, den;   // the scale, and the scale times a power of two
+          if (am >= 0x1p-60f && am <= 0x1p100f) {
+            constexpr float y = 1.0f / 448.0f;
+            const float s0 = am * y;
+            den = sc = fmaf(fmaf(-s0, 448.0f, am), y, s0);
+          } else {
+            // far from 1: the row and its scale times a power of two, exact
+            // where a code is not 0 (an infinite scale: 0, or NaN for infinities)
+            sc = __fdiv_rn(am, 448.0f);
+            const float u = am < 1.f ? 0x1p100f : isinf(sc) ? 0.f : 0x1p-60f;
+            den = isinf(sc) ? 1.f : sc * u;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float2 v = pair(x, i), q0 = mul2(v, inv2);
-          const float2 q = fma2(fma2(q0, neg2, v), inv2, q0);
-          set(x, i, make_float2(copysignf(q.x, v.x), copysignf(q.y, v.y)));   // (-0 stays -0)
-        }
-        if (live) {
-          write((kind == 1 ? a.pool.k : a.pool.v) + e);
-          if (o == 0) (kind == 1 ? a.pool.ks : a.pool.vs)[e / D] = sc;
+            for (int i = 0; i < 2 * N; ++i) x[i] *= u;
+          }
+          const float inv = __frcp_rn(den);
+          const float2 inv2 = make_float2(inv, inv), neg2 = make_float2(-den, -den);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const float2 v = pair(x, i), q0 = mul2(v, inv2);
+            const float2 q = fma2(fma2(q0, neg2, v), inv2, q0);
+            set(x, i, make_float2(copysignf(q.x, v.x), copysignf(q.y, v.y)));   // (-0 stays -0)
+          }
+          if (live) {
+            write((kind == 1 ? a.pool.k : a.pool.v) + e);
+            if (o == 0) (kind == 1 ? a.pool.ks : a.pool.vs)[e / D] = sc;
+          }
         }
       }
     }
-  }
   }
 }
 
