@@ -17,8 +17,8 @@
 // The floor is HBM (every input read once, every output written once): 8192 x 32
 // fp32 heads rotated alone take 44.6 us = 6.0 TB/s.  With norms and E4M3 pages
 // the issue slots are the bound (70 % used): 16384 tokens of 16 + 8 + 8 heads
-// 55.8 us for 36 us of bytes; with a row per warp and IEEE divisions 180 us
-// (193 instructions a row against 75).
+// 50.2 us for 36 us of bytes; with a row per warp and IEEE divisions 180 us
+// (193 instructions a row).
 //
 // E4M3 codes are RNE(x / scale) of the IEEE quotient.  The quotient comes from
 // a correctly rounded reciprocal y of the scale by one residual step
@@ -213,7 +213,8 @@ enum Mode {
 // T: element of q, k and v; TO: of q_out.  CACHE 0: rotation alone; 1: bf16
 // pages; 2: E4M3 pages.
 template <int D, typename T, typename TO, int CACHE, Mode M>
-__global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs a, int per_token) {
+__global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs a, int per_token,
+                                                                   unsigned inverse) {
   constexpr int N = D / 16;     // pairs of a lane
   constexpr int V = vector_of<T, D>(), K = 2 * N / V;
   const int lane = threadIdx.x & 31, oct = lane >> 3, o = lane & 7;
@@ -225,18 +226,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
   // `hop` apart.
   const int jobs = a.n_tokens * per_token, hop = gridDim.x * kWarps;
   const int job0 = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  // token of a job, and its first quad
+  auto token = [&](int job) { return inverse ? static_cast<int>(__umulhi(job, inverse)) : job; };
+  auto part_of = [&](int job) { return job - token(job) * per_token; };
   if (job0 >= jobs) return;
 
-  // kind of a quad: 0 q, 1 k, 2 v; this octet's head (an idle one's: the last)
-  auto kind_of = [&](int quad) { return quad < nq ? 0 : quad < nq + nk ? 1 : 2; };
-  auto head_of = [&](int quad, int kind) {
-    return 4 * (quad - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) + oct;
-  };
-  auto source = [&](int t, int kind, int head) {
-    const void* base = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-    const long long stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
-    return static_cast<const T*>(base) + t * stride + min(head, (kind == 0 ? a.Hq : a.Hkv) - 1) * D;
-  };
   // where the lane's runs start in rows that are rotated, and in others
   // (neighbours in every mode)
   int split_at[K], plain_at[K];
@@ -245,23 +239,43 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
     plain_at[k] = run_at<D, V>(false, k, o, a.rot);
     split_at[k] = M == kPairs || !a.phases ? plain_at[k] : run_at<D, V>(true, k, o, a.rot);
   }
-  Raw<T, V> raw[K];   // the next quad, across the tokens of a warp
-  int fjob = job0, ft = job0 / per_token, fquad = job0 % per_token;   // next quad to load
+  // first element of token t, and the number of heads
+  auto token_of = [&](int t, int kind) {
+    const void* base = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+    return static_cast<const T*>(base) + t * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride);
+  };
+  auto heads_of = [&](int kind) { return kind == 0 ? a.Hq : a.Hkv; };
+  // The next quad is loaded ahead, across the tokens of a warp.  Kind (0 q, 1 k,
+  // 2 v) and token change in `enter`; from quad to quad only the head moves.
+  Raw<T, V> raw[K];
+  int fjob = job0, fquad = part_of(job0);
+  int fend, flast, fhead, fat[K];   // quads of this kind end here; its last head; this octet's
+  const T* fbase;
+  auto enter = [&]() {
+    const int kind = fquad < nq ? 0 : fquad < nq + nk ? 1 : 2;
+    fend = kind == 0 ? nq : kind == 1 ? nq + nk : quads;
+    flast = heads_of(kind) - 1;
+    fhead = 4 * (fquad - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) + oct;
+    fbase = token_of(token(fjob), kind);
+#pragma unroll
+    for (int k = 0; k < K; ++k) fat[k] = kind < 2 ? split_at[k] : plain_at[k];
+  };
   auto fetch = [&]() {
     if (M == kScalar || fjob >= jobs) return;
-    const int kind = kind_of(fquad);
-    const T* p = source(ft, kind, head_of(fquad, kind));
+    const int at = min(fhead, flast) * D;   // (an idle octet takes the last head)
 #pragma unroll
-    for (int k = 0; k < K; ++k) raw[k].load(p + (kind < 2 ? split_at[k] : plain_at[k]));
+    for (int k = 0; k < K; ++k) raw[k].load(fbase + (at + fat[k]));
     fquad += per_token;
-    if (fquad >= quads) {
-      fjob += hop;
-      ft = fjob / per_token;
-      fquad = fjob % per_token;
+    fhead += 4 * per_token;
+    if (fquad >= fend) {
+      if (fquad >= quads) {
+        fjob += hop;
+        if (fjob >= jobs) return;
+        fquad = part_of(fjob);
+      }
+      enter();
     }
   };
-  fetch();
-
   // position, sequence and page of the present job and of the next one: the
   // loads of a token's place are hidden behind the rows of the one before
   struct Spot {
@@ -270,7 +284,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
   auto look = [&](int job) {
     Spot w{-1, 0, -1, 0};
     if (job < jobs) {
-      const int t = job / per_token;
+      const int t = token(job);
       w.pos = a.positions[t];
       if (CACHE) w.seq = a.seqs ? a.seqs[t] : t;
     }
@@ -287,17 +301,21 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
       w.page = a.table[static_cast<long long>(w.seq) * a.width + slot];
   };
   Spot now = look(job0), then = look(job0 + hop);
-  find(now);
-
   uint64_t phase[N / 4];
 #pragma unroll
   for (int j = 0; j < N / 4; ++j) {
     const int p = pair_at<D, V>(M != kPairs, oct * (N / 4) + j, o);
     phase[j] = a.phases && p < r ? a.phases[p] : 0;
   }
+  if constexpr (M != kScalar) {
+    enter();
+    fetch();
+  }
+
+  find(now);
 #pragma unroll 1
   for (int job = job0; job < jobs; job += hop) {
-    const int t = job / per_token, part = job % per_token;
+    const int t = token(job), part = part_of(job);
     const int pos = now.pos;
     bool keep = !CACHE || pos >= 0;   // (rotation alone: the row of padding is copied)
     long long row0 = 0;   // element of the token's row of head 0 in the pages
@@ -358,10 +376,15 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
     };
     const bool whole = 2 * r == D;   // every pair turns
 
-#pragma unroll 1
-    for (int quad = part; quad < quads; quad += per_token) {
-      const int kind = kind_of(quad), head = head_of(quad, kind);
-      const bool live = keep && head < (kind == 0 ? a.Hq : a.Hkv);
+    // the token's row in q_out and in the pages, of head 0
+    TO* const q_row = static_cast<TO*>(a.q_out) + t * a.q_out_stride;
+    uint8_t* const k_row = a.pool.k + row0 * (CACHE == 1 ? 2 : 1);
+    uint8_t* const v_row = a.pool.v + row0 * (CACHE == 1 ? 2 : 1);
+
+    // four rows of one kind, this octet's of `head`
+    auto rows = [&](auto tag, int head) {
+      constexpr int kind = decltype(tag)::value;
+      const bool live = keep && head < heads_of(kind);
       const bool loose = M == kScalar && kind < 2 && a.phases;   // element by element
       float x[2 * N];
       if constexpr (M != kScalar) {
@@ -369,7 +392,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
         for (int k = 0; k < K; ++k) raw[k].get(x + k * V);
         fetch();
       } else {
-        const T* p = source(t, kind, head);
+        const T* p = token_of(t, kind) + min(head, heads_of(kind) - 1) * D;
 #pragma unroll
         for (int i = 0; i < 2 * N; ++i) x[i] = ld1(p + (loose ? element(i) : plain_at[i / V] + i % V));
       }
@@ -450,13 +473,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
         }
       };
       if (kind == 0) {
-        if (live) write(static_cast<TO*>(a.q_out) + t * a.q_out_stride + head * D);
-        continue;
+        if (live) write(q_row + head * D);
+        return;
       }
       if constexpr (CACHE > 0) {
-        const long long e = row0 + (static_cast<long long>(head) << a.pool.shift) * D;
+        const int at = head << a.pool.shift;   // rows of the page before this one
+        uint8_t* const row = kind == 1 ? k_row : v_row;
         if constexpr (CACHE == 1) {
-          if (live) write(reinterpret_cast<uint16_t*>(kind == 1 ? a.pool.k : a.pool.v) + e);
+          if (live) write(reinterpret_cast<uint16_t*>(row) + at * D);
         } else {
           float am = 0.f;
 #pragma unroll
@@ -477,19 +501,30 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
             for (int i = 0; i < 2 * N; ++i) x[i] *= u;
           }
           const float inv = __frcp_rn(den);
-          const float2 inv2 = make_float2(inv, inv), neg2 = make_float2(-den, -den);
+          const float2 inv2 = make_float2(-inv, -inv), den2 = make_float2(den, den);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
+            // (the negative of the quotient, so that -0 stays -0)
             const float2 v = pair(x, i), q0 = mul2(v, inv2);
-            const float2 q = fma2(fma2(q0, neg2, v), inv2, q0);
-            set(x, i, make_float2(copysignf(q.x, v.x), copysignf(q.y, v.y)));   // (-0 stays -0)
+            const float2 q = fma2(fma2(q0, den2, v), inv2, q0);
+            set(x, i, make_float2(-q.x, -q.y));
           }
           if (live) {
-            write((kind == 1 ? a.pool.k : a.pool.v) + e);
-            if (o == 0) (kind == 1 ? a.pool.ks : a.pool.vs)[e / D] = sc;
+            write(row + at * D);
+            if (o == 0) (kind == 1 ? a.pool.ks : a.pool.vs)[row0 / D + at] = sc;
           }
         }
       }
+    };
+    int quad = part;
+#pragma unroll 1
+    for (; quad < nq; quad += per_token) rows(std::integral_constant<int, 0>(), 4 * quad + oct);
+    if constexpr (CACHE > 0) {
+#pragma unroll 1
+      for (; quad < nq + nk; quad += per_token) rows(std::integral_constant<int, 1>(), 4 * (quad - nq) + oct);
+#pragma unroll 1
+      for (; quad < quads; quad += per_token)
+        rows(std::integral_constant<int, 2>(), 4 * (quad - nq - nk) + oct);
     }
   }
 }
@@ -504,14 +539,17 @@ cudaError_t launch_rows(const RowsArgs& a, int sms, cudaStream_t s) {
   const int per_token = static_cast<int>(want < 1 ? 1 : want > most ? most : want);
   const long long jobs = static_cast<long long>(a.n_tokens) * per_token;
   if (jobs > (1ll << 30)) return cudaErrorInvalidValue;
+  // job / per_token = the high word of job * inverse, as jobs * per_token < 2^32
+  // (there are fewer tokens than 32 sms when per_token > 1); 0: per_token is 1
+  const unsigned inverse = per_token > 1 ? static_cast<unsigned>(((1ull << 32) + per_token - 1) / per_token) : 0;
   const long long blocks = (jobs + kWarps - 1) / kWarps;
   const unsigned n = static_cast<unsigned>(blocks < kCtas * sms ? blocks : kCtas * sms);
   if (!a.phases || a.inter)
-    rows_kernel<D, T, TO, CACHE, kPairs><<<n, kWarps * 32, 0, s>>>(a, per_token);
+    rows_kernel<D, T, TO, CACHE, kPairs><<<n, kWarps * 32, 0, s>>>(a, per_token, inverse);
   else if (a.rot % (2 * vector_of<T, D>()) == 0)
-    rows_kernel<D, T, TO, CACHE, kHalf><<<n, kWarps * 32, 0, s>>>(a, per_token);
+    rows_kernel<D, T, TO, CACHE, kHalf><<<n, kWarps * 32, 0, s>>>(a, per_token, inverse);
   else
-    rows_kernel<D, T, TO, CACHE, kScalar><<<n, kWarps * 32, 0, s>>>(a, per_token);
+    rows_kernel<D, T, TO, CACHE, kScalar><<<n, kWarps * 32, 0, s>>>(a, per_token, inverse);
   return cudaGetLastError();
 }
 
