@@ -118,7 +118,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const BeamArgs a) {
   constexpr int N = Vec<T>::N;
   __shared__ unsigned long long s_key[kRoom + kMaxK];   // gathered keys, then the best so far
-  __shared__ unsigned long long s_max[kThreads / 4];
+  __shared__ __align__(16) unsigned long long s_max[kThreads / 4];
   __shared__ unsigned long long s_bound;
   __shared__ float s_low;
   __shared__ float2 s_stat[kThreads / 32];
@@ -175,13 +175,19 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const BeamArgs a) {
     float* quads = reinterpret_cast<float*>(s_max);
     if ((lane & 3) == 0) quads[tid >> 2] = q;
     __syncthreads();
-    if (tid < kThreads / 4) {
-      const float v = quads[tid];
-      int rank = 0;
-#pragma unroll 16
-      for (int i = 0; i < kThreads / 4; ++i) rank += quads[i] > v || (quads[i] == v && i < tid);
-      if (rank == a.k - 1) s_low = v;
+    // a group's place among the 64: each of its threads compares with 16
+    int rank = 0;
+#pragma unroll
+    for (int j = 0; j < kThreads / 64; ++j) {
+      const int i = 4 * (4 * j + (lane & 3));
+      const float4 u = *reinterpret_cast<const float4*>(quads + i);
+      const float v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) rank += v[e] > q || (v[e] == q && i + e < tid >> 2);
     }
+    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+    rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+    if (rank == a.k - 1) s_low = q;   // (one group's four threads)
     __syncthreads();
   }
   const float low = s_low;
@@ -314,6 +320,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const BeamArgs a) {
     for (int i = tid; i < n; i += kThreads) {
       const unsigned long long key = s_key[i];
       int rank = 0;
+#pragma unroll 8
       for (int j = 0; j < n; ++j) rank += s_key[j] > key;
       if (rank < a.k) out[rank] = key;
     }
