@@ -342,35 +342,34 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const BeamArgs a) {
 }
 
 // The k best of a row from the sorted lists of its chunks, by one warp: a lane
-// holds the heads (and the next keys) of NL lists.
+// holds the first kAhead keys of NL lists (a list that sends more of them is
+// read on: a refill ahead of its use would have the whole warp wait for it).
+constexpr int kAhead = 4;
 template <int NL>
 __device__ __forceinline__ void merge_lists(const BeamArgs& a, const unsigned long long* lists,
                                             double own, double lse, uint32_t row0, double* sc,
-                                            uint32_t* at, const unsigned long long (&first)[4],
-                                            const unsigned long long (&second)[4]) {
+                                            uint32_t* at,
+                                            unsigned long long (&ahead)[kMaxLists / 32][kAhead]) {
   const int lane = threadIdx.x & 31;
-  unsigned long long head[NL], then[NL];
   int pos[NL];
 #pragma unroll
-  for (int i = 0; i < NL; ++i) {
-    head[i] = first[i];
-    then[i] = second[i];
-    pos[i] = 2;
-  }
+  for (int i = 0; i < NL; ++i) pos[i] = 0;
   for (int p = 0; p < a.k; ++p) {
-    unsigned long long mine = head[0];
+    unsigned long long mine = ahead[0][0];
 #pragma unroll
-    for (int i = 1; i < NL; ++i) mine = max(mine, head[i]);
+    for (int i = 1; i < NL; ++i) mine = max(mine, ahead[i][0]);
     const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(mine >> 32));
     const uint32_t lo = __reduce_max_sync(
         0xffffffffu, static_cast<uint32_t>(mine >> 32) == hi ? static_cast<uint32_t>(mine) : 0u);
     const unsigned long long best = (static_cast<unsigned long long>(hi) << 32) | lo;
 #pragma unroll
     for (int i = 0; i < NL; ++i)
-      if (head[i] == best) {   // (keys are unique; a row holds at least k)
-        head[i] = then[i];
-        then[i] = pos[i] < a.k ? __ldcg(lists + (i * 32 + lane) * a.k + pos[i]) : 0ull;
-        ++pos[i];
+      if (ahead[i][0] == best) {   // (keys are unique; a row holds at least k)
+#pragma unroll
+        for (int j = 1; j < kAhead; ++j) ahead[i][j - 1] = ahead[i][j];
+        ahead[i][kAhead - 1] = 0;
+        if (++pos[i] >= kAhead && pos[i] < a.k)
+          ahead[i][0] = __ldcg(lists + (i * 32 + lane) * a.k + pos[i]);
       }
     if (lane == 0) {
       const double v = own + static_cast<double>(logit_of(best)) - lse;
@@ -395,14 +394,14 @@ __global__ void __launch_bounds__(kMaxBeams * 32) groups_kernel(const BeamArgs a
     const double own = a.scores[r];
     const bool done = a.done && a.done[r];
     if (lane == 0) s_done[w] = done;
-    unsigned long long first[kMaxLists / 32], second[kMaxLists / 32];
+    unsigned long long ahead[kMaxLists / 32][kAhead];
     float2 t[kMaxLists / 32];
 #pragma unroll
     for (int i = 0; i < kMaxLists / 32; ++i) {
       const int c = i * 32 + lane;
       const bool has = !done && c < a.chunks;
-      first[i] = has ? __ldcg(lists + c * a.k) : 0ull;
-      second[i] = has && a.k > 1 ? __ldcg(lists + c * a.k + 1) : 0ull;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) ahead[i][j] = has && j < a.k ? __ldcg(lists + c * a.k + j) : 0ull;
       t[i] = has ? __ldcg(&a.stat[r * a.chunks + c]) : make_float2(-INFINITY, 0.f);
     }
     bool flat = !(own > -INFINITY);   // -inf or NaN: no candidate above -inf
@@ -439,9 +438,9 @@ __global__ void __launch_bounds__(kMaxBeams * 32) groups_kernel(const BeamArgs a
         }
       }
     } else if (a.chunks <= 32) {
-      merge_lists<1>(a, lists, own, lse, row0, sc, at, first, second);
+      merge_lists<1>(a, lists, own, lse, row0, sc, at, ahead);
     } else {
-      merge_lists<kMaxLists / 32>(a, lists, own, lse, row0, sc, at, first, second);
+      merge_lists<kMaxLists / 32>(a, lists, own, lse, row0, sc, at, ahead);
     }
   }
   __syncthreads();
