@@ -10,10 +10,11 @@
 // launch joins the chunks of each row, and the rows of each group, in fp64.
 //
 // The k largest of a chunk.  The k-th largest of the 64 maxima that groups of
-// four threads find in the first batch is a lower bound of the chunk's k-th
-// largest logit; what reaches it is gathered (a few times k on random logits)
-// and finds its place by counting the larger ones, so a logit costs one
-// maximum and one exponential.  Keys (order of the logit, then the lower
+// four threads find in the first two batches is a lower bound of the chunk's
+// k-th largest logit.  A thread whose batch reaches it leaves a note (and the
+// logits, while there is room), so a logit costs one maximum and one
+// exponential; the logits noted that reach the bound (a few times k of random
+// ones) find their place by counting the larger ones.  Keys (order of the logit, then the lower
 // index) are unique 64-bit words.  Where too much reaches the bound (many
 // equal logits, or -inf for most of a masked vocabulary, or rising ones), the
 // chunk is read again with keys in place of logits: the bound of every batch
@@ -40,6 +41,11 @@ constexpr int kMaxLists = 128;   // chunks of a row
 constexpr int kEach = 16;        // logits of a thread in a batch
 constexpr int kBatch = kThreads * kEach;
 constexpr int kRoom = 4 * kEach * kMaxK;   // gathered keys
+// of which the first pass uses one half; the other holds its hits
+constexpr int kKeys = kRoom / 2;
+constexpr int kHits = 2048;                // a thread and batch that reach the bound: 2 bytes
+constexpr int kKept = 64;                  // hits whose logits are kept
+static_assert(kHits * 2 + kKept * kEach * 4 <= (kRoom - kKeys) * 8, "hits");
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct BeamArgs {
@@ -117,12 +123,14 @@ struct Vec<uint16_t> {
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const BeamArgs a) {
   constexpr int N = Vec<T>::N;
-  __shared__ unsigned long long s_key[kRoom + kMaxK];   // gathered keys, then the best so far
+  __shared__ __align__(16) unsigned long long s_key[kRoom + kMaxK];   // gathered keys, then the best so far
   __shared__ __align__(16) unsigned long long s_max[kThreads / 4];
   __shared__ unsigned long long s_bound;
   __shared__ float s_low;
   __shared__ float2 s_stat[kThreads / 32];
-  __shared__ int s_n;
+  __shared__ int s_n, s_hits;
+  float (*s_val)[kEach] = reinterpret_cast<float (*)[kEach]>(s_key + kKeys);
+  uint16_t* s_hit = reinterpret_cast<uint16_t*>(s_val + kKept);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c = blockIdx.x;
   const long long r = blockIdx.y + static_cast<long long>(blockIdx.z) * gridDim.y;
@@ -165,11 +173,11 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const BeamArgs a) {
   load(0, x);
   load(1, y);   // (behind the chunk: -inf)
   if (tid == 0) {
-    s_n = 0;
+    s_n = s_hits = 0;
     s_low = -INFINITY;
   }
   {
-    float q = largest(x);
+    float q = fmaxf(largest(x), largest(y));
 #pragma unroll
     for (int o = 1; o <= 2; o <<= 1) q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, o));
     float* quads = reinterpret_cast<float*>(s_max);
@@ -195,12 +203,13 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const BeamArgs a) {
   auto use = [&](int b, const float (&v)[kEach]) {
     const float bm = largest(v);
     if (bm >= low && low > -INFINITY) {
+      const int at = atomicAdd(&s_hits, 1);
+      if (at < kHits) s_hit[at] = static_cast<uint16_t>(b * kThreads + tid);
+      if (at < kKept) {
 #pragma unroll
-      for (int e = 0; e < kEach; ++e)
-        if (v[e] >= low) {
-          const int at = atomicAdd(&s_n, 1);
-          if (at < kRoom) s_key[at] = key_of(v[e], index(b, e / N) + e % N);
-        }
+        for (int e = 0; e < kEach; e += 4)
+          *reinterpret_cast<float4*>(s_val[at] + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+      }
     }
     // (all -inf so far: the sum is 0; a NaN or +inf makes it NaN)
     if (bm > m) {
@@ -232,8 +241,23 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const BeamArgs a) {
   if (lane == 0) s_stat[warp] = make_float2(M, s);
   __syncthreads();
 
+  // the logits of the hits that reach the bound
+  const int hits = s_hits;
+  if (low > -INFINITY && hits <= kHits) {
+    for (int i = tid; i < hits * kEach; i += kThreads) {
+      const int h = i / kEach, e = i % kEach, id = s_hit[h];
+      const int at = begin + id / kThreads * kBatch + (e / N * kThreads + id % kThreads) * N + e % N;
+      const float v = h < kKept ? s_val[h][e]
+                      : at >= 0 && at < end ? Vec<T>::one(row + at) : -INFINITY;
+      if (v >= low) {
+        const int o = atomicAdd(&s_n, 1);
+        if (o < kKeys) s_key[o] = key_of(v, at);
+      }
+    }
+    __syncthreads();
+  }
   int n = s_n;
-  if (!(low > -INFINITY) || n > kRoom) {
+  if (!(low > -INFINITY) || hits > kHits || n > kKeys) {
     // Once more, by keys: the best k so far stand behind the gathered ones.
     unsigned long long* best = s_key + kRoom;
     if (tid < a.k) best[tid] = 0;
@@ -342,14 +366,13 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const BeamArgs a) {
 }
 
 // The k best of a row from the sorted lists of its chunks, by one warp: a lane
-// holds the first kAhead keys of NL lists (a list that sends more of them is
-// read on: a refill ahead of its use would have the whole warp wait for it).
-constexpr int kAhead = 4;
-template <int NL>
+// holds the first A keys of NL lists (a list that sends more of them is read
+// on: a refill ahead of its use would have the whole warp wait for it).
+template <int NL, int A>
 __device__ __forceinline__ void merge_lists(const BeamArgs& a, const unsigned long long* lists,
                                             double own, double lse, uint32_t row0, double* sc,
                                             uint32_t* at,
-                                            unsigned long long (&ahead)[kMaxLists / 32][kAhead]) {
+                                            unsigned long long (&ahead)[NL][A]) {
   const int lane = threadIdx.x & 31;
   int pos[NL];
 #pragma unroll
@@ -366,9 +389,9 @@ __device__ __forceinline__ void merge_lists(const BeamArgs& a, const unsigned lo
     for (int i = 0; i < NL; ++i)
       if (ahead[i][0] == best) {   // (keys are unique; a row holds at least k)
 #pragma unroll
-        for (int j = 1; j < kAhead; ++j) ahead[i][j - 1] = ahead[i][j];
-        ahead[i][kAhead - 1] = 0;
-        if (++pos[i] >= kAhead && pos[i] < a.k)
+        for (int j = 1; j < A; ++j) ahead[i][j - 1] = ahead[i][j];
+        ahead[i][A - 1] = 0;
+        if (++pos[i] >= A && pos[i] < a.k)
           ahead[i][0] = __ldcg(lists + (i * 32 + lane) * a.k + pos[i]);
       }
     if (lane == 0) {
@@ -379,84 +402,104 @@ __device__ __forceinline__ void merge_lists(const BeamArgs& a, const unsigned lo
   }
 }
 
-// One CTA per group, a warp per row: its sum, and its k best keys.
+// A row's sum and its k best candidates, best first, by one warp.
+template <int NL, int A>
+__device__ __forceinline__ void best_of_row(const BeamArgs& a, int w, double* sc, uint32_t* at,
+                                            bool* s_done) {
+  const int lane = threadIdx.x & 31;
+  const long long r = static_cast<long long>(blockIdx.x) * a.W + w;
+  // (loads first: the lists' heads do not wait for the row's sum)
+  const unsigned long long* lists = a.key + r * a.chunks * a.k;
+  const double own = a.scores[r];
+  const bool done = a.done && a.done[r];
+  if (lane == 0) s_done[w] = done;
+  unsigned long long ahead[NL][A];
+  float2 t[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int c = i * 32 + lane;
+    const bool has = !done && c < a.chunks;
+    t[i] = has ? __ldcg(&a.stat[r * a.chunks + c]) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int j = 0; j < A; ++j) ahead[i][j] = has && j < a.k ? __ldcg(lists + c * a.k + j) : 0ull;
+  }
+  bool flat = !(own > -INFINITY);   // -inf or NaN: no candidate above -inf
+  double lse = 0.0;
+  if (!done && !flat) {
+    float M = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) M = fmaxf(M, t[i].x);
+    M = warp_max(M);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+      sum += static_cast<double>(t[i].x == -INFINITY ? t[i].y : t[i].y * ex2((t[i].x - M) * kLog2e));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    lse = static_cast<double>(M) + log(sum);
+    // a NaN or +inf in the row, or nothing but -inf
+    flat = !(M > -INFINITY) || !(M < INFINITY) || !(sum < INFINITY);
+  }
+  const uint32_t row0 = static_cast<uint32_t>(w) * a.V;
+  if (!flat && !done) {
+    merge_lists<NL, A>(a, lists, own, lse, row0, sc, at, ahead);
+    return;
+  }
+  for (int p = lane; p < a.k; p += 32) {
+    if (flat) {
+      sc[p] = -INFINITY;
+      at[p] = row0 + p;
+    } else if (p == 0) {
+      sc[0] = own;
+      at[0] = row0 + a.eos;
+    } else {
+      sc[p] = -INFINITY;
+      at[p] = row0 + (p - 1 < a.eos ? p - 1 : p);
+    }
+  }
+}
+
+// One CTA per group: a warp per row, then one warp, a lane per row, takes the
+// best of the rows' next candidates k times.
 __global__ void __launch_bounds__(kMaxBeams * 32) groups_kernel(const BeamArgs a) {
   __shared__ double s_score[kMaxBeams * kMaxK];
   __shared__ uint32_t s_at[kMaxBeams * kMaxK];
   __shared__ bool s_done[kMaxBeams];   // (out_done may be done)
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int g = blockIdx.x;
   pdl_wait();
-  if (w < a.W) {
-    const long long r = static_cast<long long>(g) * a.W + w;
-    // (loads first: the lists' heads do not wait for the row's sum)
-    const unsigned long long* lists = a.key + r * a.chunks * a.k;
-    const double own = a.scores[r];
-    const bool done = a.done && a.done[r];
-    if (lane == 0) s_done[w] = done;
-    unsigned long long ahead[kMaxLists / 32][kAhead];
-    float2 t[kMaxLists / 32];
-#pragma unroll
-    for (int i = 0; i < kMaxLists / 32; ++i) {
-      const int c = i * 32 + lane;
-      const bool has = !done && c < a.chunks;
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) ahead[i][j] = has && j < a.k ? __ldcg(lists + c * a.k + j) : 0ull;
-      t[i] = has ? __ldcg(&a.stat[r * a.chunks + c]) : make_float2(-INFINITY, 0.f);
-    }
-    bool flat = !(own > -INFINITY);   // -inf or NaN: no candidate above -inf
-    double lse = 0.0;
-    if (!done && !flat) {
-      float M = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < kMaxLists / 32; ++i) M = fmaxf(M, t[i].x);
-      M = warp_max(M);
-      double sum = 0.0;
-#pragma unroll
-      for (int i = 0; i < kMaxLists / 32; ++i)
-        sum += static_cast<double>(t[i].x == -INFINITY ? t[i].y : t[i].y * ex2((t[i].x - M) * kLog2e));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      lse = static_cast<double>(M) + log(sum);
-      // a NaN or +inf in the row, or nothing but -inf
-      flat = !(M > -INFINITY) || !(M < INFINITY) || !(sum < INFINITY);
-    }
-    double* sc = s_score + w * a.k;
-    uint32_t* at = s_at + w * a.k;
-    const uint32_t row0 = static_cast<uint32_t>(w) * a.V;
-    if (flat || done) {
-      for (int p = lane; p < a.k; p += 32) {
-        if (flat) {
-          sc[p] = -INFINITY;
-          at[p] = row0 + p;
-        } else if (p == 0) {
-          sc[0] = own;
-          at[0] = row0 + a.eos;
-        } else {
-          sc[p] = -INFINITY;
-          at[p] = row0 + (p - 1 < a.eos ? p - 1 : p);
-        }
-      }
-    } else if (a.chunks <= 32) {
-      merge_lists<1>(a, lists, own, lse, row0, sc, at, ahead);
-    } else {
-      merge_lists<kMaxLists / 32>(a, lists, own, lse, row0, sc, at, ahead);
-    }
-  }
+  if (a.chunks <= 32)   // (one list to a lane)
+    best_of_row<1, 16>(a, w, s_score + w * a.k, s_at + w * a.k, s_done);
+  else
+    best_of_row<kMaxLists / 32, 4>(a, w, s_score + w * a.k, s_at + w * a.k, s_done);
   __syncthreads();
-  const int n = a.W * a.k;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const double v = s_score[i];
-    const uint32_t at = s_at[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += s_score[j] > v || (s_score[j] == v && s_at[j] < at);
-    if (rank >= a.k) continue;
-    const long long o = static_cast<long long>(g) * a.k + rank;
-    const int beam = at / a.V, token = at % a.V;
-    a.out_scores[o] = static_cast<float>(v);
-    a.out_parents[o] = beam;
-    a.out_tokens[o] = token;
-    if (a.out_done) a.out_done[o] = s_done[beam] || token == a.eos;
+  if (w > 0) return;
+  const bool row = lane < a.W;
+  const double* sc = s_score + lane * a.k;
+  const uint32_t* at = s_at + lane * a.k;
+  int p = 0;
+  // the order of doubles as that of integers (+ 0 makes -0 and 0 one value; 0
+  // is below -inf: no candidate)
+  auto order = [&](int p) {
+    if (!row || p >= a.k) return 0ull;
+    const unsigned long long u = __double_as_longlong(sc[p] + 0.0);
+    return u >> 63 ? ~u : u | (1ull << 63);
+  };
+  unsigned long long key = order(0);
+  for (int i = 0; i < a.k; ++i) {
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(key >> 32));
+    const uint32_t lo = __reduce_max_sync(
+        0xffffffffu, static_cast<uint32_t>(key >> 32) == hi ? static_cast<uint32_t>(key) : 0u);
+    const unsigned best =
+        __ballot_sync(0xffffffffu, key == ((static_cast<unsigned long long>(hi) << 32) | lo));
+    if (lane == __ffs(best) - 1) {   // (among equals the lowest row)
+      const long long o = static_cast<long long>(blockIdx.x) * a.k + i;
+      const int token = static_cast<int>(at[p] - static_cast<uint32_t>(lane) * a.V);
+      a.out_scores[o] = static_cast<float>(sc[p]);
+      a.out_parents[o] = lane;
+      a.out_tokens[o] = token;
+      if (a.out_done) a.out_done[o] = s_done[lane] || token == a.eos;
+      key = order(++p);
+    }
   }
 }
 

@@ -670,7 +670,9 @@ size_t dec_beam_workspace_bytes(int groups, int beams, int vocab, int k);
 /* The k best continuations of every group of beams.  Candidate (w, t) of a
  * group scores scores[w] + logits[w][t] - logsumexp(logits[w]); a beam whose
  * done flag is set has one candidate, its end token at its own score.  The k
- * highest are written best first; equal scores go to the lower w * vocab + t.
+ * highest are written best first; equal scores go to the lower w * vocab + t
+ * (the candidates of one beam keep the order of their logits, also where the
+ * sums with a huge score round to one value).
  * A score that is not a number counts as -inf (so does every candidate of a
  * row that holds a NaN or +inf, or nothing but -inf).
  *   logits       [groups * beams, vocab] of `dtype`, row_stride elements
