@@ -20,10 +20,11 @@
 // chunk is read again with keys in place of logits: the bound of every batch
 // is then exact enough that at most 64 k keys of a batch are gathered.
 //
-// Measured: 16 groups of 4 rows of 151936 fp32 logits 17.6 us (14.8 the rows,
-// 39 MB), 26.9 with a 64-bit key for every logit; one group 8.8 us.  One wave of
-// CTAs: their load, bound and gather phases coincide.  Both launches in one
-// cooperative kernel took 23 us.
+// Measured: 16 groups of 4 rows of 151936 fp32 logits 14.5 us (39 MB), 26.9 with
+// a 64-bit key for every logit; one group 7.7 us; 4 groups of 32 rows, k = 32,
+// 42 us.  One wave of CTAs: the loads alone take 7.6 us, the exponentials 1.1,
+// and their phases coincide.  Both launches in one cooperative kernel took 5 us
+// more than in two.
 #include <cuda_runtime.h>
 
 #include "dec.h"
@@ -467,10 +468,10 @@ __global__ void __launch_bounds__(kMaxBeams * 32) groups_kernel(const BeamArgs a
   __shared__ bool s_done[kMaxBeams];   // (out_done may be done)
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   pdl_wait();
-  if (a.chunks <= 32)   // (one list to a lane)
-    best_of_row<1, 16>(a, w, s_score + w * a.k, s_at + w * a.k, s_done);
+  if (a.chunks <= 32)   // (one list to a lane; 16 keys ahead cost 16 groups of 4 15.7 for 14.4 us)
+    best_of_row<1, 4>(a, w, s_score + w * a.k, s_at + w * a.k, s_done);
   else
-    best_of_row<kMaxLists / 32, 4>(a, w, s_score + w * a.k, s_at + w * a.k, s_done);
+    best_of_row<kMaxLists / 32, 2>(a, w, s_score + w * a.k, s_at + w * a.k, s_done);
   __syncthreads();
   if (w > 0) return;
   const bool row = lane < a.W;
