@@ -8,8 +8,8 @@
 // by latency; the data moves in a second, dependent launch over the whole GPU
 // (a list of (from, to, rows) that the first one leaves in the workspace),
 // bound by HBM: only the rows that a page holds are copied.  Measured: 256 of
-// 1024 pages of 1.8 MB move in 158 us = 5.9 TB/s; the bookkeeping of 64
-// sequences takes 8 us.
+// 1024 pages of 1.8 MB move in 158 us = 5.9 TB/s; a row more for each of 64
+// sequences 4.1 us, of 512 5.5 us (18 us with a warp for every sequence).
 #include <cuda_runtime.h>
 
 #include "dec.h"
@@ -63,83 +63,99 @@ __device__ __forceinline__ int block_scan(int x, int* total, int* s_warp) {
   return before + inc - x;
 }
 
+// A thread looks after a sequence (kSeqs of them); pages to be released and
+// long runs of new ones are walked by warps, from lists.
 __global__ void __launch_bounds__(kThreads) resize_kernel(const MapArgs a) {
+  constexpr int kSeqs = kMaxSeqs / kThreads;
+  constexpr int kFew = 4;            // new pages that a thread enters by itself
   __shared__ int s_warp[kWarps];
-  __shared__ int s_last[kMaxSeqs];   // page that sequence s will write into, then the one to copy
+  __shared__ int s_last[kMaxSeqs];   // page that sequence s will write into, or -1
   __shared__ int s_pref[kMaxSeqs];   // its first entry in the list of new pages
-  __shared__ int s_jobs;
+  __shared__ uint16_t s_list[kMaxSeqs];   // shrinking sequences, and from its end those of long runs
+  __shared__ int s_shrinks, s_longs, s_jobs, s_err;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = 1 << a.shift;
   const int max_rows = a.width * P;
   pdl_trigger();
+  int old[kSeqs], rows[kSeqs];   // rows now, and wanted (the same: nothing to do)
+#pragma unroll
+  for (int i = 0; i < kSeqs; ++i) {
+    const int s = tid + i * kThreads;
+    old[i] = s < a.S ? a.rows[s] : 0;
+    rows[i] = s < a.S ? a.in[s] : 0;
+    if (rows[i] < 0) rows[i] = old[i];
+  }
   if (tid == 0) {
-    s_jobs = 0;
+    s_shrinks = s_longs = s_jobs = s_err = 0;
     *a.n_jobs = 0;
   }
+  __syncthreads();
+  auto pages = [&](int n) { return (n + P - 1) >> a.shift; };
+  auto row_of = [&](int s) { return a.table + static_cast<long long>(s) * a.width; };
   // check everything before anything is changed
-  int err = 0;
-  for (int s = warp; s < a.S; s += kWarps) {
-    const int old = a.rows[s];
-    int n = a.in[s];
-    if (n < 0) n = old;
+#pragma unroll
+  for (int i = 0; i < kSeqs; ++i) {
+    const int s = tid + i * kThreads;
+    if (s >= a.S) break;
     int last = -1;
-    if (old < 0 || old > max_rows || n > max_rows) {
-      err |= DEC_DEV_BAD_POSITION;
+    if (old[i] < 0 || old[i] > max_rows || rows[i] > max_rows) {
+      atomicOr(&s_err, DEC_DEV_BAD_POSITION);
     } else {
-      const int32_t* row = a.table + static_cast<long long>(s) * a.width;
-      if (n > old && (old & (P - 1))) {
-        last = row[old >> a.shift];
-        if (last < 0 || last >= a.n_pages) err |= DEC_DEV_BAD_PAGE;
+      if (rows[i] > old[i] && (old[i] & (P - 1))) {
+        last = row_of(s)[old[i] >> a.shift];
+        if (last < 0 || last >= a.n_pages) atomicOr(&s_err, DEC_DEV_BAD_PAGE);
       }
-      for (int j = ((n + P - 1) >> a.shift) + lane; j < (old + P - 1) >> a.shift; j += 32)
-        if (row[j] < 0 || row[j] >= a.n_pages) err |= DEC_DEV_BAD_PAGE;
+      if (pages(rows[i]) < pages(old[i])) s_list[atomicAdd(&s_shrinks, 1)] = static_cast<uint16_t>(s);
     }
-    if (lane == 0) s_last[s] = last;
+    s_last[s] = last;
   }
-  const int bad_pos = __syncthreads_or(err & DEC_DEV_BAD_POSITION);
-  const int bad_page = __syncthreads_or(err & DEC_DEV_BAD_PAGE);
-  if (bad_pos || bad_page) {
-    if (tid == 0 && a.status)
-      atomicOr(a.status, (bad_pos ? DEC_DEV_BAD_POSITION : 0) | (bad_page ? DEC_DEV_BAD_PAGE : 0));
-    return;
-  }
-  // releases (`by` -1; +1 takes them back)
-  auto release = [&](int by) {
-    for (int s = warp; s < a.S; s += kWarps) {
-      const int old = a.rows[s];
-      int n = a.in[s];
-      if (n < 0 || n >= old) continue;
-      const int32_t* row = a.table + static_cast<long long>(s) * a.width;
-      for (int j = ((n + P - 1) >> a.shift) + lane; j < (old + P - 1) >> a.shift; j += 32)
-        atomicAdd(&a.refs[row[j]], by);
+  __syncthreads();
+  const int shrinks = s_shrinks;
+  // pages behind the last row of every shrinking sequence
+  auto each_freed = [&](auto visit) {
+    for (int i = warp; i < shrinks; i += kWarps) {
+      const int s = s_list[i], now = a.rows[s], n = a.in[s];
+      const int32_t* row = row_of(s);
+      for (int j = pages(n) + lane; j < pages(now); j += 32) visit(row[j]);
     }
   };
-  release(-1);
-  __syncthreads();
+  if (shrinks) {
+    each_freed([&](int page) {
+      if (page < 0 || page >= a.n_pages) atomicOr(&s_err, DEC_DEV_BAD_PAGE);
+    });
+    __syncthreads();
+  }
+  if (s_err) {
+    if (tid == 0 && a.status) atomicOr(a.status, s_err);
+    return;
+  }
+  if (shrinks) {
+    each_freed([&](int page) { atomicAdd(&a.refs[page], -1); });
+    __syncthreads();
+  }
   // copies on write, and how many new pages every sequence takes
   int need = 0;
-  for (int s0 = 0; s0 < a.S; s0 += kThreads) {
-    const int s = s0 + tid;
-    int c = 0, x = -1;
-    if (s < a.S) {
-      const int old = a.rows[s], n = a.in[s];
-      x = s_last[s];
+  unsigned copies = 0;   // bit i: sequence tid + i kThreads copies its last page
+#pragma unroll
+  for (int i = 0; i < kSeqs; ++i) {
+    if (i * kThreads >= a.S) break;
+    const int s = tid + i * kThreads;
+    int c = 0;
+    if (s < a.S && rows[i] > old[i]) {
+      const int x = s_last[s];
       if (x >= 0) {
         const int held = __ldcg(&a.refs[x]);
         int rank = 0;
         if (held > 1)
-          for (int i = 0; i < s; ++i) rank += s_last[i] == x;
-        if (rank >= held - 1) x = -1;   // the last holder keeps the page
+          for (int j = 0; j < s; ++j) rank += s_last[j] == x;
+        if (rank < held - 1) copies |= 1u << i;   // (the last holder keeps the page)
       }
-      if (n > old) c = (x >= 0) + ((n + P - 1) >> a.shift) - ((old + P - 1) >> a.shift);
+      c = ((copies >> i) & 1) + pages(rows[i]) - pages(old[i]);
     }
     int total;
     const int pre = block_scan(c, &total, s_warp);
     if (s < a.S) s_pref[s] = need + pre;
     need += total;
-    // (s_last of this slice is read by later slices as the page written into;
-    // whether it is copied goes into the sign of s_pref)
-    if (s < a.S && x >= 0) s_pref[s] = ~s_pref[s];
   }
   // the lowest free pages
   int found = 0;
@@ -157,38 +173,53 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const MapArgs a) {
   }
   __syncthreads();
   if (found < need) {
-    release(1);
+    each_freed([&](int page) { atomicAdd(&a.refs[page], 1); });
     if (tid == 0 && a.status) atomicOr(a.status, DEC_DEV_NO_PAGES);
     return;
   }
-  for (int s = warp; s < a.S; s += kWarps) {
-    const int old = a.rows[s];
-    int n = a.in[s];
-    if (n < 0 || n == old) continue;
-    int32_t* row = a.table + static_cast<long long>(s) * a.width;
-    const int have = (old + P - 1) >> a.shift, want = (n + P - 1) >> a.shift;
+  auto enter = [&](int32_t* row, int j, int at) {   // entry `at` of the list
+    const int y = __ldcg(&a.list[at]);
+    row[j] = y;
+    a.refs[y] = 1;
+    return y;
+  };
+#pragma unroll
+  for (int i = 0; i < kSeqs; ++i) {
+    const int s = tid + i * kThreads;
+    if (s >= a.S) break;
+    if (rows[i] <= old[i]) continue;
+    int32_t* row = row_of(s);
     int at = s_pref[s];
-    if (at < 0) {
-      at = ~at;
-      if (lane == 0) {
-        const int x = s_last[s], y = __ldcg(&a.list[at]);
-        row[old >> a.shift] = y;
-        a.refs[y] = 1;
-        atomicSub(&a.refs[x], 1);
-        a.jobs[atomicAdd(&s_jobs, 1)] = make_int4(x, y, old & (P - 1), 0);
-      }
-      ++at;
+    if ((copies >> i) & 1) {
+      const int x = s_last[s];
+      const int y = enter(row, old[i] >> a.shift, at++);
+      atomicSub(&a.refs[x], 1);
+      a.jobs[atomicAdd(&s_jobs, 1)] = make_int4(x, y, old[i] & (P - 1), 0);
     }
-    for (int j = have + lane; j < want; j += 32) {
-      const int y = __ldcg(&a.list[at + (j - have)]);
-      row[j] = y;
-      a.refs[y] = 1;
+    const int have = pages(old[i]), more = pages(rows[i]) - have;
+    if (more > kFew) {
+      s_pref[s] = at;
+      s_list[kMaxSeqs - 1 - atomicAdd(&s_longs, 1)] = static_cast<uint16_t>(s);
+    } else {
+      for (int j = 0; j < more; ++j) enter(row, have + j, at + j);
     }
-    for (int j = want + lane; j < have; j += 32) row[j] = -1;
-    __syncwarp();   // every lane has read rows[s]
-    if (lane == 0) a.rows[s] = n;
   }
   __syncthreads();
+  for (int i = warp; i < s_longs; i += kWarps) {
+    const int s = s_list[kMaxSeqs - 1 - i], now = a.rows[s], n = a.in[s];
+    const int have = pages(now), more = pages(n) - have;
+    for (int j = lane; j < more; j += 32) enter(row_of(s), have + j, s_pref[s] + j);
+  }
+  for (int i = warp; i < shrinks; i += kWarps) {
+    const int s = s_list[i], now = a.rows[s], n = a.in[s];
+    for (int j = pages(n) + lane; j < pages(now); j += 32) row_of(s)[j] = -1;
+  }
+  __syncthreads();   // (every warp has read the rows)
+#pragma unroll
+  for (int i = 0; i < kSeqs; ++i) {
+    const int s = tid + i * kThreads;
+    if (s < a.S && rows[i] != old[i]) a.rows[s] = rows[i];
+  }
   if (tid == 0) *a.n_jobs = s_jobs;
 }
 
@@ -380,8 +411,9 @@ MapArgs map_args(const dec_pages* p, const dec_page_map* m, void* ws, int* statu
   return a;
 }
 
+// max_jobs: pages that may have to be copied.
 cudaError_t launch_copy(const dec_pages* p, const dec_page_map* m, const MapArgs& ma, bool renumber,
-                        int sms, cudaStream_t s) {
+                        long long max_jobs, int sms, cudaStream_t s) {
   CopyArgs c{};
   c.k = static_cast<uint8_t*>(p->k);
   c.v = static_cast<uint8_t*>(p->v);
@@ -402,7 +434,9 @@ cudaError_t launch_copy(const dec_pages* p, const dec_page_map* m, const MapArgs
   c.cells = static_cast<long long>(m->n_seqs) * m->width;
   c.n_pages = p->n_pages;
   c.status = ma.status;
-  return launch_dependent(copy_kernel, dim3(16 * sms), dim3(256), 0, s, c);
+  const long long most = (max_jobs * c.L * 2 * c.H + 7) / 8;   // CTAs that could have work
+  const unsigned n = static_cast<unsigned>(most < 16 * sms ? most : 16 * sms);
+  return launch_dependent(copy_kernel, dim3(n), dim3(256), 0, s, c);
 }
 
 }  // namespace
@@ -437,7 +471,7 @@ extern "C" int dec_pages_resize(const dec_pages* pool, const dec_page_map* map,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   resize_kernel<<<1, kThreads, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_copy(pool, map, a, false, sms, s);
+  if (e == cudaSuccess) e = launch_copy(pool, map, a, false, map->n_seqs, sms, s);
   return e == cudaSuccess ? DEC_OK : cuda_failed(e);
 }
 
@@ -453,7 +487,7 @@ extern "C" int dec_pages_compact(const dec_pages* pool, const dec_page_map* map,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   compact_kernel<<<1, kThreads, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_copy(pool, map, a, true, sms, s);
+  if (e == cudaSuccess) e = launch_copy(pool, map, a, true, pool->n_pages, sms, s);
   return e == cudaSuccess ? DEC_OK : cuda_failed(e);
 }
 
@@ -466,8 +500,9 @@ extern "C" int dec_pages_fork(const dec_pages* pool, const dec_page_map* map,
   if (!is_aligned(parents, 4) || !is_aligned(status, 4)) return DEC_ERR_ALIGN;
   MapArgs a = map_args(pool, map, nullptr, status);
   a.in = parents;
-  int cols = kForkCells / a.S;
-  cols = cols > 16 ? 16 : cols;
+  // 8 cells to a thread, as far as columns allow
+  int cols = 8 * kForkThreads / a.S;
+  cols = cols > 16 ? 16 : cols < 1 ? 1 : cols;
   const int slices = (a.width + cols - 1) / cols;
   fork_kernel<<<slices + 1, kForkThreads, 0, static_cast<cudaStream_t>(stream)>>>(a, cols);
   const cudaError_t e = cudaGetLastError();

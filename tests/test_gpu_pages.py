@@ -185,6 +185,30 @@ def test_many_sequences():
     same(c, m, pools, host)
 
 
+@pytest.mark.parametrize("n", [300, 1025, 2500])
+def test_sequences_shrink_and_grow_by_many_pages_at_once(n):
+    """Every kind of change in one call: freed, cropped, kept, grown by a row (a
+    copy where the page is shared), by a few pages and by many."""
+    width = 9
+    c, m, pools, host = make(n * 6, n, width, 8, layers=1, kv=1, seed=n)
+    rng = random.Random(n)
+    t = [rng.choice([0, 3, 8, 20, 41]) for _ in range(n)]
+    assert m.resize(t)
+    c.resize(i32(t))
+    par = [s // 2 * 2 if s % 3 else s for s in range(n)]
+    m.fork(par), c.fork(i32(par))
+    for _ in range(3):
+        t = [rng.choice([0, r // 2, -1, r, min(72, r + 1), min(72, r + 30), 72]) for r in m.rows]
+        if not m.resize(t):
+            c.resize(i32(t))
+            assert c.check() == capi.DEC_DEV_NO_PAGES
+        else:
+            c.resize(i32(t))
+            assert c.check() == 0
+            m.move(*host)
+        same(c, m, pools, host)
+
+
 def test_nested_layout_moves_only_its_pages():
     """Pages outermost, K and V of all layers in one buffer."""
     g = torch.Generator().manual_seed(12)
