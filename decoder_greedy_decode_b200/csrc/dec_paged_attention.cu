@@ -182,7 +182,7 @@ struct Cfg {
   // 2K to 4K rows: 95 us, 118 with 2).  bf16 heads of 128 want the registers of
   // 2 (32 sequences of 16K to 32K rows: 458 us, 496 with 3)
   static constexpr int CTAS = !FP8 && D == 128 ? 2 : 3;
-  static constexpr int ROOM = (227 * 1024 / CTAS - 3072) / kWarps;   // a warp's share
+  static constexpr int ROOM = (227 * 1024 / CTAS - 3 * 1024) / kWarps;   // a warp's share
   static constexpr int S = ROOM / (2 * HB + SB) < 8 ? ROOM / (2 * HB + SB) : 8;  // ring slots
   static constexpr int SMEM = 1024 + kWarps * S * (2 * HB + SB);
 };
