@@ -68,6 +68,32 @@ def test_selection(G, W, V, k, dtype):
     assert all(torch.equal(u, v) for u, v in zip(b, again))
 
 
+@pytest.mark.parametrize("k", [1, 8, 32])
+@pytest.mark.parametrize("order", ["random", "rising", "late"])
+def test_many_rows_of_one_long_chunk(k, order):
+    """Enough rows that a CTA takes each whole: thousands of logits reach the
+    first bound, or the largest ones all come late."""
+    G, W, V = 40, 8, 120007
+    g = torch.Generator(device="cuda").manual_seed(k)
+    x = torch.randn((G, W, V), generator=g, device="cuda")
+    if order == "rising":
+        x = x.sort(-1).values
+    elif order == "late":
+        x[..., V // 2:] += 1.5      # about a tenth of the second half
+    scores = -3 * torch.rand((G, W), generator=g, device="cuda")
+    r = beam.beam_select(x, scores, k=k)
+    lse = torch.stack([row.double().logsumexp(-1) for row in x.unbind(0)])
+    # the scores are those of the candidates named, and the k largest there are
+    at = x[torch.arange(G, device="cuda")[:, None], r.parents.long(), r.tokens.long()].double()
+    own = (scores.double() - lse).gather(1, r.parents.long()) + at
+    bound = LSE + 2.0 ** -24 * own.abs()
+    assert bool(((r.scores.double() - own).abs() <= bound).all())
+    best = (x.topk(k, -1).values.double() + (scores.double() - lse)[..., None]).flatten(1).topk(k, -1).values
+    assert bool(((own - best).abs() <= 4 * LSE).all())
+    named = r.parents.long() * V + r.tokens
+    assert all(len(set(row)) == k for row in named.tolist())
+
+
 def test_ties_go_to_the_lowest_index():
     x = torch.zeros((2, 3, 20000))
     x[1, :, 777] = 1.0
