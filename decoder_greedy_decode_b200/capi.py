@@ -96,7 +96,8 @@ class dec_append(ctypes.Structure):
                 ("v_stride", ctypes.c_longlong), ("q_out", ctypes.c_void_p),
                 ("positions", ctypes.c_void_p), ("seqs", ctypes.c_void_p),
                 ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
-                ("eps", ctypes.c_float), ("rope", ctypes.POINTER(dec_rope))]
+                ("eps", ctypes.c_float), ("rope", ctypes.POINTER(dec_rope)),
+                ("zero_skipped", ctypes.c_int)]
 
 
 class DecError(RuntimeError):

@@ -49,6 +49,7 @@ struct RowsArgs {
   const int32_t *positions, *seqs;
   const uint16_t *q_norm, *k_norm;
   float eps;
+  int zero;                           // q_out rows of skipped tokens: 1 = zeroed
   const uint64_t* phases;             // null: no rotation
   int rot, inter;
   float mscale;
@@ -473,7 +474,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rows_kernel(const RowsArgs
         }
       };
       if (kind == 0) {
-        if (live) write(q_row + head * D);
+        if (live) {
+          write(q_row + head * D);
+        } else if (CACHE && !keep && a.zero && head < a.Hq) {
+#pragma unroll
+          for (int i = 0; i < 2 * N; ++i) x[i] = 0.f;
+          write(q_row + head * D);
+        }
         return;
       }
       if constexpr (CACHE > 0) {
@@ -690,6 +697,7 @@ extern "C" int dec_paged_append(const dec_pages* pool, const dec_page_map* map, 
   a.q_norm = static_cast<const uint16_t*>(io->q_norm);
   a.k_norm = static_cast<const uint16_t*>(io->k_norm);
   a.eps = io->eps;
+  a.zero = io->zero_skipped != 0;
   if (io->rope) {
     a.phases = io->rope->phases;
     a.rot = io->rope->rot_dim;

@@ -161,8 +161,8 @@ class PagedKV:
         """Store the rows k, v [tokens, n_kv_heads, head_dim] of new tokens at
         `positions` of sequences `seqs` (int32; None: token i is sequence i),
         k normalised by k_norm and rotated by `rope`, and q [tokens,
-        n_q_heads, head_dim] likewise into q_out (bf16; zeros if None), which
-        is returned.  Tokens at negative positions are skipped."""
+        n_q_heads, head_dim] likewise into q_out (bf16; a new one, zero
+        where tokens are skipped, if None), which is returned.  Tokens at negative positions are skipped."""
         dev = self.device
         if tensors.elsewhere(dev, stream):
             with tensors.guard(dev, stream):
@@ -179,7 +179,8 @@ class PagedKV:
             if shape[0] != T or shape[2] != D or q.dtype != k.dtype:
                 raise ValueError(f"q must be [{T}, heads, {D}] of {k.dtype}")
             if q_out is None:
-                q_out = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
+                q_out = q.new_empty(shape, dtype=torch.bfloat16)
+                io.zero_skipped = 1
             else:
                 tensors.check_tensor(q_out, "q_out", torch.bfloat16, shape, dev)
             io.n_q_heads, io.q, io.q_stride = shape[1], q.data_ptr(), q.stride(0)

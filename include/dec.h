@@ -613,6 +613,7 @@ typedef struct dec_append {
                                * or NULL for none */
   float eps;
   const dec_rope *rope;       /* HOST struct, or NULL for no rotation */
+  int zero_skipped;           /* 1: q_out rows of skipped tokens become 0; 0: left */
 } dec_append;
 
 /* Store the keys and values of new tokens in the pages of one layer, the keys
@@ -625,7 +626,8 @@ typedef struct dec_append {
  * pairs must be distinct: a row named twice holds elements of either token.
  * A token whose sequence is out of range or whose page is not assigned
  * raises DEC_DEV_BAD_PAGE, a position behind the table's end
- * DEC_DEV_BAD_POSITION; such a token is skipped whole.  map->rows and
+ * DEC_DEV_BAD_POSITION; such a token is skipped whole (see zero_skipped for its
+ * row of q_out).  map->rows and
  * map->refs are not used.  Asynchronous on `stream`. */
 int dec_paged_append(const dec_pages *pool, const dec_page_map *map, int layer,
                      const dec_append *io, int *status, void *stream);

@@ -271,3 +271,27 @@ def test_append_replays_in_a_graph():
     g.replay()
     assert torch.equal(q_out, c.append(0, k, v, pos, rope=rope, q=q))
 
+
+
+@pytest.mark.parametrize("D,R", [(64, 64), (128, 128), (128, 20)])
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_a_new_q_out_is_zero_where_tokens_are_skipped(D, R, fmt):
+    c = PagedKV.create(1, 4, 8, 2, D, 2, 16, dtype=fmt)
+    c.resize(torch.tensor([8, 3], dtype=torch.int32).cuda())
+    g = torch.Generator().manual_seed(D + R)
+    q = torch.randn((70, 5, D), generator=g).bfloat16().cuda()
+    k = torch.randn((70, 2, D), generator=g).bfloat16().cuda()
+    pos, seqs = torch.full((70,), -1, dtype=torch.int32), torch.zeros(70, dtype=torch.int32)
+    pos[3], pos[40], pos[41], pos[69] = 2, 15, 1, 4      # row 15 has no page
+    seqs[41], seqs[69] = 1, 7                            # there is no sequence 7
+    rope = Rope(R, theta=1e4)
+    torch.empty((70, 5, D), dtype=torch.bfloat16, device="cuda").fill_(9.0)   # (its memory may come back)
+    out = c.append(0, k, k, pos.cuda(), seqs=seqs.cuda(), rope=rope, q=q)
+    assert c.check() == capi.DEC_DEV_BAD_PAGE
+    done = torch.zeros(70, dtype=torch.bool)
+    done[[3, 41]] = True
+    assert bool((out[~done] == 0).all()) and bool((out[done] != 0).any(-1).all())
+    kept = torch.full_like(out, 9.0)
+    c.append(0, k, k, pos.cuda(), seqs=seqs.cuda(), rope=rope, q=q, q_out=kept)
+    assert torch.equal(kept[done], out[done]) and bool((kept[~done] == 9).all())
+    c.check()
