@@ -9,7 +9,7 @@
 // (a list of (from, to, rows) that the first one leaves in the workspace),
 // bound by HBM: only the rows that a page holds are copied.  Measured: 256 of
 // 1024 pages of 1.8 MB move in 158 us = 5.9 TB/s; a row more for each of 64
-// sequences 4.1 us, of 512 5.5 us (18 us with a warp for every sequence).
+// sequences 3.5 us, of 512 4.7 us (18 us with a warp for every sequence).
 #include <cuda_runtime.h>
 
 #include "dec.h"
@@ -65,7 +65,7 @@ __device__ __forceinline__ int block_scan(int x, int* total, int* s_warp) {
 
 // A thread looks after a sequence (kSeqs of them); pages to be released and
 // long runs of new ones are walked by warps, from lists.
-__global__ void __launch_bounds__(kThreads) resize_kernel(const MapArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) resize_kernel(const MapArgs a) {
   constexpr int kSeqs = kMaxSeqs / kThreads;
   constexpr int kFew = 4;            // new pages that a thread enters by itself
   __shared__ int s_warp[kWarps];
