@@ -23,8 +23,8 @@
 // cp.async of the same rings (32 sequences of 16K to 32K rows).
 //
 // Measured (16 query heads on 8 KV heads of 128): 32 x 16K to 32K rows 470 us
-// (6.8 TB/s); 64 x 2K to 4K rows E4M3 79 us (5.3 TB/s; loads alone 67: the
-// conversions' issue and latency are in the way); 64 x 200 to 420 rows 20.6 us
+// (6.8 TB/s); 64 x 2K to 4K rows E4M3 75.5 us (5.5 TB/s; loads alone 67, the
+// barrier and the joins 4); 64 x 200 to 420 rows 20.6 us
 // (4.0 TB/s; loads alone 15.7, the barrier 1.6, the joins 2); 795 rows 8.9 us
 // (latencies: length, page ids, rows, barrier, join).
 //
@@ -481,6 +481,8 @@ __device__ __forceinline__ void run_tiles(const PagedArgs& a, const CUtensorMap&
     const int r0 = row0<TR>(cp);
     // a tile at an end of the sequence holds rows that are not part of it
     // (anything may stand there): their p is 0 and their V is made 0
+    // (once for all blocks of a tile: branches among the blocks keep their
+    // instructions apart, 79 against 75.5 us for 64 x 2K to 4K rows E4M3)
     const bool edge = r0 < cp.lo || r0 + TR > cp.len;
     auto in = [&](int r) { return r0 + r >= cp.lo && r0 + r < cp.len; };
     // scores of block n: rows 16 n + ra (x 0, 1) and 8 further (x 2, 3), heads
@@ -531,7 +533,10 @@ __device__ __forceinline__ void run_tiles(const PagedArgs& a, const CUtensorMap&
       x[n][1] = (s[0][1] + s[1][1]) * (sc1 * ks0);
       x[n][2] = (s[0][2] + s[1][2]) * (sc0 * ks1);
       x[n][3] = (s[0][3] + s[1][3]) * (sc1 * ks1);
-      if (edge) {
+    }
+    if (edge) {
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
         if (!in(16 * n + ra)) {
           x[n][0] = x[n][1] = -INFINITY;
           vs[n][0] = 0.f;
@@ -541,6 +546,9 @@ __device__ __forceinline__ void run_tiles(const PagedArgs& a, const CUtensorMap&
           vs[n][1] = 0.f;
         }
       }
+    }
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
       t0 = fmaxf(t0, fmaxf(x[n][0], x[n][2]));
       t1 = fmaxf(t1, fmaxf(x[n][1], x[n][3]));
     }
@@ -660,11 +668,17 @@ __device__ __forceinline__ void run_tiles(const PagedArgs& a, const CUtensorMap&
             v[n][e][0] = u.x;
             v[n][e][1] = u.y;
           }
-          if (edge && !in(16 * n + (e / 2) * 8 + (e & 1 ? v1 : v0))) {
-#pragma unroll
-            for (int i = 0; i < W; ++i) v[n][e][i] = 0;
-          }
         }
+      if (edge) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!in(16 * n + (e / 2) * 8 + (e & 1 ? v1 : v0))) {
+#pragma unroll
+              for (int i = 0; i < W; ++i) v[n][e][i] = 0;
+            }
+      }
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         if constexpr (!FP8) {
