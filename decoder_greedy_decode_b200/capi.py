@@ -39,7 +39,9 @@ EXPORTS = (
     "dec_init_int8", "dec_quantize_int8", "dec_init_fp8w", "dec_quantize_fp8w",
     "dec_rope_phases", "dec_rope_apply", "dec_pages_workspace_bytes", "dec_pages_resize",
     "dec_pages_fork", "dec_pages_compact", "dec_paged_append",
-    "dec_paged_attention_workspace_bytes", "dec_paged_attention", "dec_beam_workspace_bytes",
+    "dec_paged_attention_workspace_bytes", "dec_paged_attention",
+    "dec_paged_attention_set_timeout_ns", "dec_paged_attention_set_debug_stall",
+    "dec_beam_workspace_bytes",
     "dec_beam_select", "dec_kv_reorder", "dec_beam_backtrace",
 )
 #: the projections an int8 handle holds as int8 codes + row scales
@@ -159,6 +161,8 @@ def lib() -> ctypes.CDLL:
             "dec_paged_append": ([PG, PM, I, AP, P, P], I),
             "dec_paged_attention_workspace_bytes": ([PG, I, I], Z),
             "dec_paged_attention": ([PG, PM, I, I, I, P, S, P, I, P, P, P, Z, P, P], I),
+            "dec_paged_attention_set_timeout_ns": ([U64], I),
+            "dec_paged_attention_set_debug_stall": ([I], I),
             "dec_beam_workspace_bytes": ([I, I, I, I], Z),
             "dec_beam_select": ([I, I, I, I, I, P, S, P, P, I, P, P, P, P, P, Z, P], I),
             "dec_kv_reorder": ([I, I, I, I, I, I, P, P, I, P, P, P, P], I),
@@ -396,6 +400,15 @@ def dec_paged_attention(pool: dec_pages, pmap: dec_page_map, layer: int, batch: 
                                   _ptr(q), q_stride, _ptr(rows), window, _ptr(out), _ptr(lse),
                                   _ptr(workspace), workspace_bytes, _ptr(status),
                                   _stream(stream)), "dec_paged_attention")
+
+
+def dec_paged_attention_set_timeout_ns(ns: int) -> None:
+    _ok(lib().dec_paged_attention_set_timeout_ns(ns), "dec_paged_attention_set_timeout_ns")
+
+
+def dec_paged_attention_set_debug_stall(warp_plus_one: int) -> None:
+    _ok(lib().dec_paged_attention_set_debug_stall(warp_plus_one),
+        "dec_paged_attention_set_debug_stall")
 
 
 def dec_beam_workspace_bytes(groups: int, beams: int, vocab: int, k: int) -> int:

@@ -79,6 +79,8 @@ struct PagedArgs {
   float* part;     // [warps][2] states: rep x D sums, then rep x (m, l)
   int2* desc;      // [B] (first worker, workers) whose states are joined
   int* status;
+  unsigned long long timeout_ns;   // bound of a wait for copies
+  int stall;       // warp of the grid that withholds its first copies (tests), or -1
 };
 
 // c += a b; with FIRST, c = a b.
@@ -223,9 +225,10 @@ __device__ __forceinline__ void next(const PagedArgs& a, Place& p) {
 // Row of an octet that M index i stands for.
 __device__ __forceinline__ int row_of(int i) { return i ^ ((i & 1) << 2); }
 
-// This warp's run of tiles.
+// This warp's run of tiles.  True if copies may still be on their way into the
+// ring (a wait ran out, and so did the wait for the rest).
 template <int D, bool FP8>
-__device__ __forceinline__ void run_tiles(const PagedArgs& a, const CUtensorMap& kmap,
+__device__ __forceinline__ bool run_tiles(const PagedArgs& a, const CUtensorMap& kmap,
                                           const CUtensorMap& vmap) {
   using C = Cfg<D, FP8>;
   constexpr int S = C::S, NS = C::NS, TR = C::TR, ES = C::ES, HB = C::HB, TB = 2 * HB;
@@ -270,7 +273,7 @@ __device__ __forceinline__ void run_tiles(const PagedArgs& a, const CUtensorMap&
   }
   const long long run = (total + workers - 1) / workers;
   const long long first = worker * run;
-  if (worker >= workers || first >= total) return;
+  if (worker >= workers || first >= total) return false;
   const int count = static_cast<int>(min(run, total - first));
   long long base = 0;   // tiles before the sequence that holds the first one
   Place ip;
@@ -338,7 +341,7 @@ __device__ __forceinline__ void run_tiles(const PagedArgs& a, const CUtensorMap&
         }
     }
     bad = (bad & ~(1u << slot)) | (wrong << slot);
-    if (lane == 0) {
+    if (lane == 0 && (me != a.stall || issued > 0)) {
       uint64_t* bar = &s_bar[warp][slot];
       const uint32_t dst = ring + slot * TB, sdst = scales + slot * C::SB;
       constexpr int row_total = 2 * D * ES + (FP8 ? 8 : 0);   // bytes of a K and V row
@@ -783,17 +786,31 @@ __device__ __forceinline__ void run_tiles(const PagedArgs& a, const CUtensorMap&
     }
   };
 
+  // Whether the copies of tile i have landed within the limit.  One answer for
+  // the warp: lanes that part ways here would miss each other's shuffles.
+  auto landed = [&](int i, Spin1& sp) {
+    bool ok = false;
+    while (!(ok = mbar_wait(&s_bar[warp][i % S], (i / S) & 1, kWaitHintNs)) && !sp.expired()) {
+    }
+    return __all_sync(0xffffffffu, ok) != 0;
+  };
   start();
-  bool late = false;   // a wait ran out: the results are not written
+  // A wait ran out: nothing of this run is written from here on, and nothing
+  // more is copied.  Copies in flight get the limit once more to land.
+  bool late = false, stuck = false;
   for (int i = 0; i < count; ++i) {
-    if (!late) issue();
     const int slot = i % S;
-    Spin1 sp;
-    while (!mbar_wait(&s_bar[warp][slot], (i / S) & 1, kWaitHintNs))
-      if (late || sp.expired()) {
-        late = true;
-        break;
+    if (!late) {
+      issue();
+      Spin1 sp;
+      sp.limit_ns = a.timeout_ns;
+      late = !landed(i, sp);
+      if (late) {
+        Spin1 rest;
+        rest.limit_ns = a.timeout_ns;
+        for (int j = i; j < issued; ++j) stuck |= !landed(j, rest);
       }
+    }
     if (late || ((bad >> slot) & 1)) {
       poison = true;
       if (a.status && lane == 0) atomicOr(a.status, late ? DEC_DEV_TIMEOUT : DEC_DEV_BAD_PAGE);
@@ -807,6 +824,7 @@ __device__ __forceinline__ void run_tiles(const PagedArgs& a, const CUtensorMap&
       if (last) start();
     }
   }
+  return stuck;
 }
 
 // Joins the states of one (sequence, query head); also the outputs of empty
@@ -971,7 +989,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) paged_kernel(
   __shared__ Item s_many[kWarps];
   __shared__ int s_n;
   if (threadIdx.x == 0) s_n = 0;
-  run_tiles<D, FP8>(a, kmap, vmap);
+  // (copies that may still land would overwrite the weights of join_by_cta)
+  const bool stuck = __syncthreads_or(run_tiles<D, FP8>(a, kmap, vmap)) != 0;
   cooperative_groups::this_grid().sync();
   const int lane = threadIdx.x & 31;
   const long long items = static_cast<long long>(a.B) * a.Hq;
@@ -989,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, FP8>::CTAS) paged_kernel(
     }
     __syncthreads();
     const int n = s_n;
-    for (int i = 0; i < n; ++i) join_by_cta<D>(a, s_many[i], reinterpret_cast<float*>(smem_raw));
+    for (int i = 0; i < n && !stuck; ++i) join_by_cta<D>(a, s_many[i], reinterpret_cast<float*>(smem_raw));
     if (n) {   // (join_by_cta may end early for a poisoned sequence)
       __syncthreads();
       if (threadIdx.x == 0) s_n = 0;
@@ -1035,6 +1054,9 @@ EncodeTiledFn encode_tiled() {
   }
   return reinterpret_cast<EncodeTiledFn>(f);
 }
+
+std::atomic<unsigned long long> g_timeout_ns{2000000000ull};
+std::atomic<int> g_stall{-1};
 
 int tile_rows(const dec_pages* p) {
   if (p->dtype == DEC_KV_FP8_E4M3) return p->head_dim == 128 ? Cfg<128, true>::TR : Cfg<64, true>::TR;
@@ -1129,6 +1151,8 @@ extern "C" int dec_paged_attention(const dec_pages* pool, const dec_page_map* ma
   a.part = static_cast<float*>(workspace);
   a.desc = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + state_bytes(grid, a.rep, D));
   a.status = status;
+  a.timeout_ns = g_timeout_ns.load(std::memory_order_relaxed);
+  a.stall = g_stall.load(std::memory_order_relaxed);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   const EncodeTiledFn enc = encode_tiled();
@@ -1142,4 +1166,16 @@ extern "C" int dec_paged_attention(const dec_pages* pool, const dec_page_map* ma
     e = D == 128 ? launch_paged<128, false>(a, km, vm, grid, s)
                  : launch_paged<64, false>(a, km, vm, grid, s);
   return e == cudaSuccess ? DEC_OK : cuda_failed(e);
+}
+
+extern "C" int dec_paged_attention_set_timeout_ns(unsigned long long ns) {
+  if (ns < 1000000ull) return DEC_ERR_ARG;
+  g_timeout_ns.store(ns, std::memory_order_relaxed);
+  return DEC_OK;
+}
+
+extern "C" int dec_paged_attention_set_debug_stall(int warp_plus_one) {
+  if (warp_plus_one < 0) return DEC_ERR_ARG;
+  g_stall.store(warp_plus_one - 1, std::memory_order_relaxed);
+  return DEC_OK;
 }

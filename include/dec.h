@@ -654,12 +654,23 @@ size_t dec_paged_attention_workspace_bytes(const dec_pages *pool, int batch, int
  * their mix.  rows[b] < 0 or behind the table's end raises
  * DEC_DEV_BAD_POSITION, an unassigned page DEC_DEV_BAD_PAGE; that sequence's
  * outputs (of the KV heads concerned) are left as they were.  map->refs is
- * not used.  Asynchronous on `stream` (one cooperative launch of a grid that
- * fills the GPU). */
+ * not used.  A copy of rows that does not arrive within the limit (2 s, or
+ * dec_paged_attention_set_timeout_ns) raises DEC_DEV_TIMEOUT: any of the call's
+ * outputs may then be as they were, those that are written are right.
+ * Asynchronous on `stream` (one cooperative launch of a grid that fills the
+ * GPU). */
 int dec_paged_attention(const dec_pages *pool, const dec_page_map *map, int layer, int batch,
                         int n_q_heads, const void *q, long long q_stride, const int32_t *rows,
                         int window, float *out, float *lse, void *workspace,
                         size_t workspace_bytes, int *status, void *stream);
+
+/* Bound of the waits of dec_paged_attention, in nanoseconds (at least 1e6), for
+ * the calls of this process that follow (captured ones keep theirs). */
+int dec_paged_attention_set_timeout_ns(unsigned long long ns);
+
+/* Test hook: 0 = normal; k > 0 makes warp k-1 of the grids that follow withhold
+ * the copies of its first tile, so that its wait runs out (without any fault). */
+int dec_paged_attention_set_debug_stall(int warp_plus_one);
 
 /* ------------------------------------------------------------------ */
 /* Beam search                                                         */
