@@ -38,7 +38,7 @@ EXPORTS = (
     "dec_attention_noalloc", "dec_verify", "dec_accept_greedy", "dec_generate",
     "dec_init_int8", "dec_quantize_int8", "dec_init_fp8w", "dec_quantize_fp8w",
     "dec_rope_phases", "dec_rope_apply", "dec_pages_workspace_bytes", "dec_pages_resize",
-    "dec_pages_fork", "dec_pages_compact", "dec_paged_append",
+    "dec_pages_fork", "dec_pages_compact", "dec_status_take", "dec_paged_append",
     "dec_paged_attention_workspace_bytes", "dec_paged_attention",
     "dec_paged_attention_set_timeout_ns", "dec_paged_attention_set_debug_stall",
     "dec_beam_workspace_bytes",
@@ -158,6 +158,7 @@ def lib() -> ctypes.CDLL:
             "dec_pages_resize": ([PG, PM, P, P, Z, P, P], I),
             "dec_pages_fork": ([PG, PM, P, P, P], I),
             "dec_pages_compact": ([PG, PM, P, P, Z, P, P], I),
+            "dec_status_take": ([P, P, P], I),
             "dec_paged_append": ([PG, PM, I, AP, P, P], I),
             "dec_paged_attention_workspace_bytes": ([PG, I, I], Z),
             "dec_paged_attention": ([PG, PM, I, I, I, P, S, P, I, P, P, P, Z, P, P], I),

@@ -374,6 +374,9 @@ __global__ void __launch_bounds__(256) copy_kernel(const CopyArgs a) {
   }
 }
 
+// A bit that another stream's kernel raises meanwhile is in *out or stays.
+__global__ void take_status_kernel(int* status, int* out) { *out = atomicExch(status, 0); }
+
 struct Layout {
   size_t list, list2, remap, jobs, total;
 };
@@ -505,6 +508,14 @@ extern "C" int dec_pages_fork(const dec_pages* pool, const dec_page_map* map,
   cols = cols > 16 ? 16 : cols < 1 ? 1 : cols;
   const int slices = (a.width + cols - 1) / cols;
   fork_kernel<<<slices + 1, kForkThreads, 0, static_cast<cudaStream_t>(stream)>>>(a, cols);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? DEC_OK : cuda_failed(e);
+}
+
+extern "C" int dec_status_take(int* status, int* out, void* stream) {
+  if (!status || !out) return DEC_ERR_NULL;
+  if (!is_aligned(status, 4) || !is_aligned(out, 4)) return DEC_ERR_ALIGN;
+  take_status_kernel<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>(status, out);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? DEC_OK : cuda_failed(e);
 }

@@ -246,8 +246,15 @@ class PagedKV:
 
     def check(self) -> int:
         """The device errors since the last check (DEC_DEV_* bits; waits for
-        the work on the current stream)."""
-        code = int(self.status.item())
-        if code:
-            self.status.zero_()
-        return code
+        the work on the current stream).  An error that a call on another
+        stream finds meanwhile is in this check's bits or in the next one's."""
+        dev = self.device
+        if tensors.elsewhere(dev, None):
+            with tensors.guard(dev, None):
+                return self.check()
+        taken = torch.empty(1, dtype=torch.int32, device=dev)
+        rc = capi.lib().dec_status_take(self._status, taken.data_ptr(),
+                                        tensors.current_stream_of(dev))
+        if rc:
+            raise capi.DecError(rc, "dec_status_take")
+        return int(taken.item())

@@ -595,6 +595,12 @@ int dec_pages_fork(const dec_pages *pool, const dec_page_map *map, const int32_t
 int dec_pages_compact(const dec_pages *pool, const dec_page_map *map, int32_t *n_live,
                       void *workspace, size_t workspace_bytes, int *status, void *stream);
 
+/* Move the bits of a status word (the `status` of the calls of this section and
+ * the next) to *out (device int) and clear it, as one atomic step: a bit that a
+ * call on another stream raises meanwhile is in *out or in *status.
+ * Asynchronous on `stream`. */
+int dec_status_take(int *status, int *out, void *stream);
+
 /* One call's rows for dec_paged_append.  q, k and v are [n_tokens, heads,
  * head_dim] of `dtype` with their own element strides between tokens (slices
  * of one projection's output are fine), 16-byte aligned, strides multiples
