@@ -24,7 +24,7 @@ class Rope:
     scaling      "none", "linear", "ntk" or "parts" (dec_rope_scaling), with
                  `factor`; "parts" needs `orig_ctx` and takes alpha, beta
     mscale       factor of the rotated elements; by default 1, and for "parts"
-                 0.1 ln(factor) + 1
+                 0.1 ln(factor) + 1 where factor is above 1
     """
 
     def __init__(self, rot_dim: int, theta: float = 1e6, interleaved: bool = False,
@@ -37,7 +37,7 @@ class Rope:
         capi.dec_rope_phases(rot_dim, theta, SCALINGS[scaling], factor, orig_ctx, alpha, beta, host)
         self.rot_dim, self.interleaved = rot_dim, bool(interleaved)
         if mscale is None:
-            mscale = 0.1 * math.log(factor) + 1.0 if scaling == "parts" else 1.0
+            mscale = 0.1 * math.log(max(factor, 1.0)) + 1.0 if scaling == "parts" else 1.0
         self.mscale = float(mscale)
         bits = [p - (1 << 64) if p >= (1 << 63) else p for p in host]
         self.phases = torch.tensor(bits, dtype=torch.int64).to(device)
