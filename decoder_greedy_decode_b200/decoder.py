@@ -164,6 +164,11 @@ class Decoder:
             raise ValueError(f"{G} groups of {W} beams need a handle and a cache for {G * W} sequences")
         if n_steps < 1:
             raise ValueError("n_steps must be at least 1")
+        # (what the selection would refuse: before the cache is written)
+        if capi.dec_beam_workspace_bytes(G, W, V, W) == 0:
+            raise ValueError(f"{W} beams over a vocabulary of {V} are not supported")
+        if not -1 <= eos < V:
+            raise ValueError(f"eos must be a token of the vocabulary or -1, got {eos}")
         with torch.cuda.device(dev):
             tok = token_ids.repeat_interleave(W)
             pos = positions.repeat_interleave(W)
