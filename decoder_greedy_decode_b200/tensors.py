@@ -52,6 +52,9 @@ class guard:
     there and scratch allocated within belongs to that stream."""
 
     def __init__(self, device, stream):
+        on = getattr(stream, "device", None)   # (None: a raw handle, taken to be of `device`)
+        if on is not None and on != device:
+            raise ValueError(f"the stream must be one of {device}, got one of {on}")
         self.device, self.stream = device, stream
 
     def __enter__(self):
