@@ -353,54 +353,12 @@ def dec_rope_phases(rot_dim: int, theta: float, scaling: int, factor: float, ori
                               ctypes.cast(phases_host, ctypes.c_void_p)), "dec_rope_phases")
 
 
-def dec_rope_apply(n_tokens: int, n_heads: int, head_dim: int, dtype: int, x, x_stride: int, out,
-                   out_stride: int, positions, rope: dec_rope, stream=None) -> None:
-    _ok(lib().dec_rope_apply(n_tokens, n_heads, head_dim, dtype, _ptr(x), x_stride, _ptr(out),
-                             out_stride, _ptr(positions), ctypes.byref(rope), _stream(stream)),
-        "dec_rope_apply")
-
-
 def dec_pages_workspace_bytes(pool: dec_pages, pmap: dec_page_map) -> int:
     return int(lib().dec_pages_workspace_bytes(ctypes.byref(pool), ctypes.byref(pmap)))
 
 
-def dec_pages_resize(pool: dec_pages, pmap: dec_page_map, new_rows, workspace,
-                     workspace_bytes: int, status=None, stream=None) -> None:
-    _ok(lib().dec_pages_resize(ctypes.byref(pool), ctypes.byref(pmap), _ptr(new_rows),
-                               _ptr(workspace), workspace_bytes, _ptr(status), _stream(stream)),
-        "dec_pages_resize")
-
-
-def dec_pages_fork(pool: dec_pages, pmap: dec_page_map, parents, status=None,
-                   stream=None) -> None:
-    _ok(lib().dec_pages_fork(ctypes.byref(pool), ctypes.byref(pmap), _ptr(parents), _ptr(status),
-                             _stream(stream)), "dec_pages_fork")
-
-
-def dec_pages_compact(pool: dec_pages, pmap: dec_page_map, n_live, workspace,
-                      workspace_bytes: int, status=None, stream=None) -> None:
-    _ok(lib().dec_pages_compact(ctypes.byref(pool), ctypes.byref(pmap), _ptr(n_live),
-                                _ptr(workspace), workspace_bytes, _ptr(status), _stream(stream)),
-        "dec_pages_compact")
-
-
-def dec_paged_append(pool: dec_pages, pmap: dec_page_map, layer: int, io: dec_append, status=None,
-                     stream=None) -> None:
-    _ok(lib().dec_paged_append(ctypes.byref(pool), ctypes.byref(pmap), layer, ctypes.byref(io),
-                               _ptr(status), _stream(stream)), "dec_paged_append")
-
-
 def dec_paged_attention_workspace_bytes(pool: dec_pages, batch: int, n_q_heads: int) -> int:
     return int(lib().dec_paged_attention_workspace_bytes(ctypes.byref(pool), batch, n_q_heads))
-
-
-def dec_paged_attention(pool: dec_pages, pmap: dec_page_map, layer: int, batch: int,
-                        n_q_heads: int, q, q_stride: int, rows, window: int, out, lse, workspace,
-                        workspace_bytes: int, status=None, stream=None) -> None:
-    _ok(lib().dec_paged_attention(ctypes.byref(pool), ctypes.byref(pmap), layer, batch, n_q_heads,
-                                  _ptr(q), q_stride, _ptr(rows), window, _ptr(out), _ptr(lse),
-                                  _ptr(workspace), workspace_bytes, _ptr(status),
-                                  _stream(stream)), "dec_paged_attention")
 
 
 def dec_paged_attention_set_timeout_ns(ns: int) -> None:
@@ -414,23 +372,6 @@ def dec_paged_attention_set_debug_stall(warp_plus_one: int) -> None:
 
 def dec_beam_workspace_bytes(groups: int, beams: int, vocab: int, k: int) -> int:
     return int(lib().dec_beam_workspace_bytes(groups, beams, vocab, k))
-
-
-def dec_beam_select(groups: int, beams: int, vocab: int, k: int, dtype: int, logits,
-                    row_stride: int, scores, done, eos: int, out_scores, out_parents, out_tokens,
-                    out_done, workspace, workspace_bytes: int, stream=None) -> None:
-    _ok(lib().dec_beam_select(groups, beams, vocab, k, dtype, _ptr(logits), row_stride,
-                              _ptr(scores), _ptr(done), eos, _ptr(out_scores), _ptr(out_parents),
-                              _ptr(out_tokens), _ptr(out_done), _ptr(workspace), workspace_bytes,
-                              _stream(stream)), "dec_beam_select")
-
-
-def dec_kv_reorder(n_layers: int, n_kv_heads: int, head_dim: int, dtype: int, kv_batch: int,
-                   max_ctx: int, values, scales, batch: int, parents, rows, status=None,
-                   stream=None) -> None:
-    _ok(lib().dec_kv_reorder(n_layers, n_kv_heads, head_dim, dtype, kv_batch, max_ctx,
-                             _ptr(values), _ptr(scales), batch, _ptr(parents), _ptr(rows),
-                             _ptr(status), _stream(stream)), "dec_kv_reorder")
 
 
 def dec_beam_backtrace(n_steps: int, groups: int, beams: int, parents, tokens, out,

@@ -79,8 +79,3 @@ def elsewhere(device, stream) -> bool:
 def current_stream_of(device) -> int:
     """The raw current stream of `device`."""
     return _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
-
-
-def failed(code: int, what: str) -> None:
-    """Raise the error of a library call that did not return 0."""
-    raise capi.DecError(code, what)
