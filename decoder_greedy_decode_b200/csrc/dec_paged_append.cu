@@ -3,9 +3,11 @@
 //
 // Mathematics.  Pair i of a rotated head turns by p * f_i at position p.  The
 // angle is kept in turns as a 64-bit binary fraction: p * phase_i modulo 2^64
-// drops whole turns exactly, so the angle of any int32 position is right to
-// 2^-33 turns (a product in fp32 is off by p * f_i * 2^-24 radians, i.e. by
-// 0.06 rad at p = 2^20).  The rotation itself is fp32, rounded once.
+// drops whole turns exactly, so the product is right to 2^-33 turns at any int32
+// position (in fp32 it is off by p * f_i * 2^-24 radians, i.e. by 0.06 rad at
+// p = 2^20).  Its top 32 bits (cut: 2^-32 turns) become fp32 half turns for the
+// sine and cosine, rounded by at most 2^-26 turns, 1e-7 rad: what fp32 operands
+// near a half turn hold.  The rotation itself is fp32, rounded once.
 //
 // Split.  A warp takes tokens, and the head rows of each four at a time:
 // eight lanes hold a row, 16 (head_dim 128) or 8 (64) of its elements each, so
@@ -16,9 +18,10 @@
 // for all rows.  The next rows are loaded before the present ones are used.
 // The floor is HBM (every input read once, every output written once): 8192 x 32
 // fp32 heads rotated alone take 45.1 us = 5.9 TB/s.  With norms and E4M3 pages
-// the issue slots are the bound (70 % used): 16384 tokens of 16 + 8 + 8 heads
-// 50.2 us for 36 us of bytes; with a row per warp and IEEE divisions 180 us
-// (193 instructions a row).
+// issue is the bound: two thirds of the slots are used, the rest is lost to
+// fixed latencies with the 20 warps an SM that the registers allow.  16384 tokens
+// of 16 + 8 + 8 heads 50.2 us for 36 us of bytes; with a row per warp and IEEE
+// divisions 180 us (193 instructions a row).
 //
 // E4M3 codes are RNE(x / scale) of the IEEE quotient.  The quotient comes from
 // a correctly rounded reciprocal y of the scale by one residual step

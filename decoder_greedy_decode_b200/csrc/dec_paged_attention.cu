@@ -46,9 +46,15 @@
 // one accumulator would drift (1.2e-5 of the output at 24K rows).  E4M3 codes
 // are exact in f16 and stay codes: the K scale multiplies the score, the V
 // scale multiplies p, whose planes are then f16 after a power-of-two factor F
-// per head that keeps the largest p * scale near 2^14 (2^-22 relative, values
+// per head that keeps the largest p * scale near 2^14 (2^-23 relative, values
 // below 2^-39 of the largest lost).  q is made f16 by a power of two per
-// head, exact down to 2^-38 of the head's largest element.
+// head: elements down to 2^-31 of the head's largest are exact (8 bits above
+// f16's smallest step, 2^-24, with the largest in [2^14, 2^15)), smaller ones are
+// off by at most 2^-39 of it.
+//
+// Waits.  Every wait for copies has a limit.  Whether it ran out is one decision
+// of the warp, which then copies nothing more, lets what is in flight land (the
+// limit once more) and marks its states, so that the joins leave those outputs.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -7,9 +7,10 @@
 // (tables and counts: a few hundred KB at most) runs in one CTA and is bound
 // by latency; the data moves in a second, dependent launch over the whole GPU
 // (a list of (from, to, rows) that the first one leaves in the workspace),
-// bound by HBM: only the rows that a page holds are copied.  Measured: 256 of
-// 1024 pages of 1.8 MB move in 158 us = 5.9 TB/s; a row more for each of 64
-// sequences 3.5 us, of 512 4.7 us (18 us with a warp for every sequence).
+// bound by HBM: a copy on write moves the filled rows of its page, a compaction
+// whole pages.  Measured: 256 of 1024 pages of 1.8 MB move in 158 us = 5.9 TB/s;
+// a row more for each of 64 sequences 3.5 us, of 512 4.7 us (18 us with a warp
+// for every sequence).
 #include <cuda_runtime.h>
 
 #include "dec.h"

@@ -154,8 +154,10 @@ class Decoder:
         Returns (sequences int32 [groups, beams, n_steps], scores fp32 [groups,
         beams], the sums of log probabilities), best first.  A beam that emits
         eos is finished: it keeps its score and repeats eos.  Sequence
-        g * beams + w of `kv` ends with the rows of beam w.  Errors found on
-        the device as in step (check)."""
+        g * beams + w of `kv` ends with the rows of beam w.  All n_steps run,
+        on the current stream, whether or not beams finish: positions[g] +
+        n_steps may not pass the cache's max_ctx.  Errors found on the device
+        as in step (check), the results are then of no use."""
         G, W, V = int(token_ids.numel()), beams, self.shape.vocab
         dev = kv.buf.device
         tensors.check_tensor(token_ids, "token_ids", torch.int32, (G,), dev)

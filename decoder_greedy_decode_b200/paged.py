@@ -213,7 +213,8 @@ class PagedKV:
                stream=None):
         """Attention of one new token per sequence: q bf16 [batch, n_q_heads,
         head_dim] over the first rows[b] rows (int32; None: self.rows) of
-        sequences 0 .. batch-1, the last `window` of them if that is not 0.
+        sequences 0 .. batch-1, the last `window` of them if that is not 0
+        (several new tokens of one sequence have no call of their own yet).
         Returns out fp32 [batch, n_q_heads, head_dim], with return_lse also
         the log of the softmax sums [batch, n_q_heads]."""
         dev = self.device

@@ -80,7 +80,8 @@ typedef enum dec_status {
    * dec_check(); the step that saw them wrote -1 to every out_ids entry */
   DEC_DEV_BAD_POSITION = 1,   /* a position < 0 or >= max_ctx */
   DEC_DEV_BAD_TOKEN = 2,      /* a token id < 0 or >= vocab */
-  DEC_DEV_TIMEOUT = 4,        /* a bounded device wait ran out (see dec_set_timeout_ns) */
+  DEC_DEV_TIMEOUT = 4,        /* a bounded device wait ran out (see dec_set_timeout_ns,
+                               * dec_paged_attention_set_timeout_ns) */
   /* raised in the `status` argument of the paged-cache and beam calls */
   DEC_DEV_BAD_PAGE = 8,       /* a page id, sequence or parent out of range */
   DEC_DEV_NO_PAGES = 16       /* too few free pages */
@@ -506,8 +507,10 @@ typedef struct dec_rope {
  *              out may be x (same stride); otherwise they do not overlap
  *   positions  int32 [n_tokens] (device); the row of a token whose position
  *              is negative (padding) is copied as it is
- * The angle is exact to 2^-33 turns at any position, the rotation is fp32,
- * rounded once to `dtype`.  head_dim 64 or 128 (DEC_ERR_SHAPE); x and out
+ * Position times phase is exact to 2^-33 turns at any position; its top 32
+ * bits are made fp32 for the sine and cosine, so the angle that turns is
+ * within 2^-26 + 2^-32 turns (1e-7 radians).  The rotation is fp32, rounded
+ * once to `dtype`.  head_dim 64 or 128 (DEC_ERR_SHAPE); x and out
  * 16-byte aligned (DEC_ERR_ALIGN).  Asynchronous on `stream`. */
 int dec_rope_apply(int n_tokens, int n_heads, int head_dim, int dtype, const void *x,
                    long long x_stride, void *out, long long out_stride,
@@ -703,8 +706,10 @@ size_t dec_beam_workspace_bytes(int groups, int beams, int vocab, int k);
  *                the group); out_tokens int32 [groups, k]; out_done uint8
  *                [groups, k] (done before, or the token is eos), may be NULL.
  *                With k = beams, out_scores may be scores and out_done done.
- * beams 1..32, k 1..32, k <= vocab <= 1000000.  Scores are summed and compared in fp64
- * and rounded once.  Asynchronous on `stream`. */
+ * beams 1..32, k 1..32, k <= vocab <= 1000000.  The sum of a row's
+ * exponentials is fp32 within the chunks that the row is cut into and joined in
+ * fp64; scores are added and compared in fp64 and rounded once.  Asynchronous on
+ * `stream`. */
 int dec_beam_select(int groups, int beams, int vocab, int k, int dtype, const void *logits,
                     long long row_stride, const float *scores, const uint8_t *done, int eos,
                     float *out_scores, int32_t *out_parents, int32_t *out_tokens,
