@@ -52,8 +52,8 @@ class guard:
     there and scratch allocated within belongs to that stream."""
 
     def __init__(self, device, stream):
-        on = getattr(stream, "device", None)   # (None: a raw handle, taken to be of `device`)
-        if on is not None and on != device:
+        on = getattr(stream, "device", None)   # (a raw or foreign handle is taken to be of `device`)
+        if isinstance(on, torch.device) and on != device:
             raise ValueError(f"the stream must be one of {device}, got one of {on}")
         self.device, self.stream = device, stream
 
